@@ -74,6 +74,7 @@ typedef enum {
 #define PKV_DEVERR_INDPTR 0x8           /* qo_indptr not monotone / prefix < 0 */
 #define PKV_DEVERR_TABLE_IDX_RANGE 0x10 /* table_idx negative                  */
 #define PKV_DEVERR_TIMEOUT 0x20         /* a bounded in-kernel wait gave up     */
+#define PKV_DEVERR_POSITION 0x40        /* a position outside the cos/sin table */
 
 /* The KV pool (one tensor, see the layout above). base: device, bf16,
  * 16-byte aligned. Passed by pointer; the library does not keep it. */
@@ -111,6 +112,42 @@ const char *pkv_last_error(void);
 pkv_status pkv_kv_store(const pkv_pool *pool, int32_t layer, const void *k, const void *v,
                         int64_t kv_row_stride, const int32_t *out_loc, int64_t num_tokens,
                         cudaStream_t stream);
+
+/*
+ * A step's q and k normed and rotated, and its k and v appended to the pool,
+ * in one launch (what a model runs between the QKV projection and the
+ * attention calls below; pkv_kv_store takes k and v that are already so).
+ * For t < num_tokens and every q and k head x (fp32, rounded once at the end):
+ *   x = x * rsqrt(mean(x^2) + eps) * weight        with q_norm (k_norm)
+ *   (a, b) = (a cos - b sin, b cos + a sin)        for its rot_dim / 2 pairs:
+ *     (x[m], x[m + rot_dim / 2]), or (x[2m], x[2m + 1]) if interleaved; dims
+ *     from rot_dim on are not rotated
+ *   q_out[t] = q[t],  pool[0 | 1, layer, out_loc[t]] = k[t] | v[t]
+ * q: device bf16 [num_tokens, num_q_heads, D], token rows q_row_stride
+ * elements apart; k, v: [num_tokens, Hkv, D], kv_row_stride apart (strides at
+ * least a row and multiples of 8, heads and dims contiguous, 16-byte aligned:
+ * all three may be column slices of one fused projection output). q_out:
+ * contiguous [num_tokens, num_q_heads, D]; it may be q itself if q is
+ * contiguous, and may not overlap q, k or v otherwise, nor any of them the
+ * pool. num_q_heads 0: q and q_out are not used (append only).
+ * q_norm, k_norm: device bf16 [D], 16-byte aligned, or NULL (no norm). eps >= 0.
+ * cos_sin: device fp32 [num_positions, rot_dim], 16-byte aligned, the cosines
+ * of the rot_dim / 2 angles of each position, then their sines. rot_dim: a
+ * multiple of 16, at most D, or 0 (no rotation; cos_sin and positions unused).
+ * positions, out_loc: device int32 [num_tokens]. A token whose position is
+ * outside the table is skipped (PKV_DEVERR_POSITION: its q_out row is not
+ * written either); one whose slot is outside the pool is not stored, only its
+ * q_out row is written (PKV_DEVERR_OUT_LOC_RANGE). Two tokens with the same
+ * slot give an unspecified one of the two rows. v's bits are copied unchanged.
+ */
+pkv_status pkv_norm_rope_kv_store(const pkv_pool *pool, int32_t layer, const void *q,
+                                  int64_t q_row_stride, void *q_out, int32_t num_q_heads,
+                                  const void *k, const void *v, int64_t kv_row_stride,
+                                  const void *q_norm, const void *k_norm, float eps,
+                                  const float *cos_sin, int64_t num_positions, int32_t rot_dim,
+                                  int32_t interleaved, const int32_t *positions,
+                                  const int32_t *out_loc, int64_t num_tokens,
+                                  cudaStream_t stream);
 
 /*
  * Bytes of device workspace pkv_paged_decode_attn needs for these host-side

@@ -60,6 +60,10 @@ def load() -> ctypes.CDLL:
     L.pkv_last_error.restype = ctypes.c_char_p
     L.pkv_kv_store.restype = ctypes.c_int
     L.pkv_kv_store.argtypes = [pool_p, _c_int32, _p, _p, _c_int64, _p, _c_int64, _p]
+    L.pkv_norm_rope_kv_store.restype = ctypes.c_int
+    L.pkv_norm_rope_kv_store.argtypes = [pool_p, _c_int32, _p, _c_int64, _p, _c_int32, _p, _p,
+                                         _c_int64, _p, _p, ctypes.c_float, _p, _c_int64,
+                                         _c_int32, _c_int32, _p, _p, _c_int64, _p]
     L.pkv_decode_workspace_size.restype = ctypes.c_size_t
     L.pkv_decode_workspace_size.argtypes = [_c_int32] * 5
     L.pkv_paged_decode_attn.restype = ctypes.c_int
@@ -131,6 +135,23 @@ def _contig(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _one_device(*tensors):
+    """Every tensor (None: skipped) lives on the current device, where the kernels run."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a [N, heads, D] tensor whose rows are contiguous."""
+    s0, s1, s2 = t.stride()
+    _, h, d = t.shape
+    if s2 != 1 or (s1 != d and h != 1):
+        raise ValueError(f"{name} must have its heads and dims contiguous")
+    return s0 if t.shape[0] != 1 else h * d
+
+
 def pool_struct(pool: torch.Tensor) -> PkvPool:
     """Descriptor of a (2, layers, pages, page_size, kv_heads, head_dim) bf16 pool."""
     _want(pool, torch.bfloat16, "pool", 6)
@@ -160,6 +181,56 @@ def pkv_kv_store(pool, layer: int, k, v, out_loc, stream=None) -> None:
         raise ValueError("k and v rows must share a row stride with heads/dims contiguous")
     _check(load().pkv_kv_store(ctypes.byref(ps), int(layer), _ptr(k), _ptr(v), k.stride(0),
                                _ptr(out_loc), n, _stream(stream)))
+
+
+def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc, cos_sin=None,
+                           q_norm=None, k_norm=None, eps: float = 1e-6,
+                           interleaved: bool = False, stream=None) -> None:
+    """Norm and rotate q [N, Hq, D] into q_out (contiguous; q itself if q is) and k [N, Hkv, D],
+    append k and v to the pool at out_loc [N]; rows may be strided (slices of a fused projection).
+    cos_sin [positions, rot_dim] fp32, cosines first, or None (no rotation: positions may be None);
+    q_norm, k_norm [D] bf16 weights or None. q and q_out None: append only."""
+    ps = pool_struct(pool)
+    n, hkv, d = k.shape
+    if hkv != ps.num_kv_heads or d != ps.head_dim or v.shape != k.shape:
+        raise ValueError("k and v must be [N, Hkv, D] with the pool's heads and dims")
+    for t, name in ((k, "k"), (v, "v")):
+        _want(t, torch.bfloat16, name, 3)
+    ks = _row_stride(k, "k")
+    if _row_stride(v, "v") != ks:
+        raise ValueError("k and v rows must share a row stride")
+    _want(out_loc, torch.int32, "out_loc", 1)
+    _contig(out_loc, "out_loc")
+    if out_loc.shape[0] != n:
+        raise ValueError("out_loc must have one slot per token")
+    hq = qs = 0
+    if q is not None:
+        _want(q, torch.bfloat16, "q", 3)
+        _want(q_out, torch.bfloat16, "q_out", 3)
+        _contig(q_out, "q_out")
+        if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [N, Hq, D] with k's tokens and dims")
+        hq, qs = q.shape[1], _row_stride(q, "q")
+    rot = table = 0
+    if cos_sin is not None:
+        _want(cos_sin, torch.float32, "cos_sin", 2)
+        _contig(cos_sin, "cos_sin")
+        _want(positions, torch.int32, "positions", 1)
+        _contig(positions, "positions")
+        table, rot = cos_sin.shape
+        if positions.shape[0] != n:
+            raise ValueError("positions must have one entry per token")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _want(w, torch.bfloat16, name, 1)
+            _contig(w, name)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must have head_dim entries")
+    _one_device(pool, k, v, out_loc, q, q_out, cos_sin, positions if rot else None, q_norm, k_norm)
+    _check(load().pkv_norm_rope_kv_store(
+        ctypes.byref(ps), int(layer), _ptr(q), qs, _ptr(q_out), hq, _ptr(k), _ptr(v), ks,
+        _ptr(q_norm), _ptr(k_norm), float(eps), _ptr(cos_sin), table, rot, int(bool(interleaved)),
+        _ptr(positions) if rot else None, _ptr(out_loc), n, _stream(stream)))
 
 
 def pkv_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -156,6 +156,100 @@ pkv_status pkv_kv_store(const pkv_pool *pool, int32_t layer, const void *k, cons
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "kv_store launch");
 }
 
+// Byte range of n rows of `width` elements, `stride` elements apart.
+struct Span {
+  uintptr_t lo, hi;
+};
+static Span rows_span(const void *p, int64_t n, int64_t stride, int64_t width) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + 2 * static_cast<uintptr_t>((n - 1) * stride + width)};
+}
+static bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+
+pkv_status pkv_norm_rope_kv_store(const pkv_pool *pool, int32_t layer, const void *q,
+                                  int64_t q_row_stride, void *q_out, int32_t num_q_heads,
+                                  const void *k, const void *v, int64_t kv_row_stride,
+                                  const void *q_norm, const void *k_norm, float eps,
+                                  const float *cos_sin, int64_t num_positions, int32_t rot_dim,
+                                  int32_t interleaved, const int32_t *positions,
+                                  const int32_t *out_loc, int64_t num_tokens,
+                                  cudaStream_t stream) {
+  pkv::PoolGeom g;
+  pkv_status s = check_pool(pool, layer, &g);
+  if (s != PKV_OK) return s;
+  if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_q_heads < 0) return fail(PKV_ERR_INVALID_ARG, "num_q_heads < 0");
+  if (rot_dim < 0 || rot_dim > g.d || rot_dim % 16 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "rot_dim %d must be a multiple of 16 in [0, %d]", rot_dim, g.d);
+  if (!isfinite(eps) || eps < 0.f) return fail(PKV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (num_tokens == 0) return PKV_OK;
+  if (num_tokens > 0x7fffffff)
+    return fail(PKV_ERR_UNSUPPORTED, "num_tokens %lld past 2^31 - 1",
+                static_cast<long long>(num_tokens));
+  if (!k || !v || !out_loc) return fail(PKV_ERR_INVALID_ARG, "k, v and out_loc must be non-NULL");
+  if (num_q_heads > 0 && (!q || !q_out))
+    return fail(PKV_ERR_INVALID_ARG, "q and q_out must be non-NULL with q heads");
+  if (rot_dim > 0 && (!cos_sin || !positions || num_positions <= 0))
+    return fail(PKV_ERR_INVALID_ARG, "a rotation needs positions and a non-empty cos_sin table");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16) ||
+      (num_q_heads > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) ||
+      (rot_dim > 0 && !aligned(cos_sin, 16)))
+    return fail(PKV_ERR_INVALID_ARG, "q, q_out, k, v, norms and cos_sin must be 16-byte aligned");
+  if (!aligned(out_loc, 4) || (rot_dim > 0 && !aligned(positions, 4)))
+    return fail(PKV_ERR_INVALID_ARG, "int32 tables must be 4-byte aligned");
+  const int64_t kv_row = static_cast<int64_t>(g.hkv) * g.d;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * g.d;
+  if (kv_row_stride < kv_row || kv_row_stride % 8 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "kv_row_stride %lld must be >= Hkv*D and a multiple of 8",
+                static_cast<long long>(kv_row_stride));
+  const Span sp{reinterpret_cast<uintptr_t>(g.base),
+                reinterpret_cast<uintptr_t>(g.base) +
+                    4 * static_cast<uintptr_t>(g.num_layers) * static_cast<uintptr_t>(g.plane)};
+  const Span sk = rows_span(k, num_tokens, kv_row_stride, kv_row);
+  const Span sv = rows_span(v, num_tokens, kv_row_stride, kv_row);
+  if (overlap(sk, sp) || overlap(sv, sp))
+    return fail(PKV_ERR_INVALID_ARG, "k and v may not overlap the pool");
+  if (num_q_heads > 0) {
+    if (q_row_stride < q_row || q_row_stride % 8 != 0)
+      return fail(PKV_ERR_INVALID_ARG, "q_row_stride %lld must be >= Hq*D and a multiple of 8",
+                  static_cast<long long>(q_row_stride));
+    const Span sq = rows_span(q, num_tokens, q_row_stride, q_row);
+    const Span so = rows_span(q_out, num_tokens, q_row, q_row);
+    if (overlap(sq, sp) || overlap(so, sp))
+      return fail(PKV_ERR_INVALID_ARG, "q and q_out may not overlap the pool");
+    if (overlap(so, sk) || overlap(so, sv) ||
+        (overlap(so, sq) && !(q_out == q && q_row_stride == q_row)))
+      return fail(PKV_ERR_INVALID_ARG, "q_out may not overlap q, k or v (or be a contiguous q itself)");
+  }
+  DevInfo *d = nullptr;
+  if ((s = device_info(&d)) != PKV_OK) return s;
+  pkv::NormRopeArgs a{};
+  a.pool = static_cast<__nv_bfloat16 *>(const_cast<void *>(g.base));
+  a.plane = g.plane;
+  a.slots = g.slots;
+  a.num_layers = g.num_layers;
+  a.layer = layer;
+  a.hkv = g.hkv;
+  a.hq = num_q_heads;
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.q_stride = q_row_stride;
+  a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  a.k = static_cast<const __nv_bfloat16 *>(k);
+  a.v = static_cast<const __nv_bfloat16 *>(v);
+  a.kv_stride = kv_row_stride;
+  a.q_norm = num_q_heads > 0 ? static_cast<const __nv_bfloat16 *>(q_norm) : nullptr;
+  a.k_norm = static_cast<const __nv_bfloat16 *>(k_norm);
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.rot_dim = rot_dim;
+  a.positions = positions;
+  a.out_loc = out_loc;
+  a.err = d->err;
+  cudaError_t e = pkv::launch_norm_rope_store(g, a, num_tokens, interleaved != 0, stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm_rope_kv_store launch");
+}
+
 size_t pkv_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, int32_t max_seq_len_hint) {
   if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||

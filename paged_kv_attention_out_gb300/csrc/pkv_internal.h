@@ -2,6 +2,7 @@
 // kernel translation units. Arguments arrive here already validated.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -39,6 +40,34 @@ DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d
 cudaError_t launch_kv_store(const PoolGeom &g, int32_t layer, const void *k, const void *v,
                             int64_t row_stride, const int32_t *out_loc, int64_t n,
                             int32_t sm_count, unsigned *err, cudaStream_t stream);
+
+// Norm + rotation of q and k, append of k and v (norm_rope.cu). n < 2^31 tokens.
+struct NormRopeArgs {
+  __nv_bfloat16 *pool;
+  int64_t plane;
+  int64_t slots;
+  int32_t num_layers;
+  int32_t layer;
+  int32_t hkv;
+  int32_t hq;  // 0: append only
+  const __nv_bfloat16 *q;
+  int64_t q_stride;
+  __nv_bfloat16 *q_out;  // may be q itself
+  const __nv_bfloat16 *k;
+  const __nv_bfloat16 *v;
+  int64_t kv_stride;
+  const __nv_bfloat16 *q_norm;  // [D] or null
+  const __nv_bfloat16 *k_norm;
+  float eps;
+  const float *cos_sin;  // [num_positions, rot_dim]: cosines, then sines
+  int64_t num_positions;
+  int32_t rot_dim;  // 0: no rotation, else a multiple of 16
+  const int32_t *positions;
+  const int32_t *out_loc;
+  unsigned *err;
+};
+cudaError_t launch_norm_rope_store(const PoolGeom &g, const NormRopeArgs &a, int64_t n,
+                                   bool interleaved, cudaStream_t stream);
 
 cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void *o, float *lse,
                           const int32_t *page_table, int64_t table_stride,
