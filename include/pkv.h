@@ -75,6 +75,7 @@ typedef enum {
 #define PKV_DEVERR_TABLE_IDX_RANGE 0x10 /* table_idx negative                  */
 #define PKV_DEVERR_TIMEOUT 0x20         /* a bounded in-kernel wait gave up     */
 #define PKV_DEVERR_POSITION 0x40        /* a position outside the cos/sin table */
+#define PKV_DEVERR_TREE 0x80            /* a draft tree too large, or a parent not an earlier token */
 
 /* The KV pool (one tensor, see the layout above). base: device, bf16,
  * 16-byte aligned. Passed by pointer; the library does not keep it. */
@@ -325,6 +326,57 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
                                        int32_t max_seq_len_hint, int64_t max_total_keys_hint,
                                        void *workspace, size_t workspace_bytes,
                                        cudaStream_t stream);
+
+/* Most drafted tokens a request may have in pkv_paged_tree_attn. */
+#define PKV_MAX_TREE_TOKENS 256
+
+/*
+ * Bytes of device workspace pkv_paged_tree_attn needs for these host-side
+ * sizes on the current device: fp32 states of the requests whose keys are
+ * shared by several CTAs (0 where nothing can be; about 40 MB at most, plus
+ * 8 bytes per request). 0 for invalid sizes. max_tree_tokens: a bound on the
+ * drafted tokens of a request, 1 .. PKV_MAX_TREE_TOKENS; max_seq_len_hint: a
+ * bound on every seq_len (>= 1).
+ */
+size_t pkv_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t max_tree_tokens,
+                               int32_t max_seq_len_hint);
+
+/*
+ * Attention of drafted tokens over the cache (speculative decoding: one call
+ * scores a tree of drafts per request). Request r owns the drafted tokens
+ * qo_indptr[r] .. qo_indptr[r+1]-1 of q (c_r of them, at most
+ * max_tree_tokens); seq_lens[r] counts its cached keys plus the drafted ones,
+ * whose keys and values are already stored at positions p_r = seq_lens[r] -
+ * c_r .. seq_lens[r] - 1 of its row (pkv_kv_store, pkv_norm_rope_kv_store).
+ * parents: device int32 [total_q], for drafted token j of a request the index
+ * among its drafted tokens of the one it continues (an earlier one, < j), or
+ * -1 if it continues the last cached token. Token j attends to
+ *   keys 0 .. p_r - 1, and keys p_r + i for i = j and every ancestor i of j;
+ *   o[t,h,:], lse[t,h] = attention of q[t,h,:] over those keys (as decode).
+ * A chain (parents[j] = j - 1) gives the causal mask of pkv_paged_extend_attn.
+ * q, o, lse, qo_indptr, page_table, table_idx, seq_lens as for extend;
+ * Hq / Hkv <= 16. workspace: device, 256-byte aligned, at least
+ * pkv_tree_workspace_size(batch, Hq, Hkv, D, max_tree_tokens,
+ * max_seq_len_hint) bytes, contents irrelevant on entry (two calls that can
+ * overlap on the GPU need one each). max_seq_len_hint < 1: the row capacity
+ * table_stride * page_size; a longer request is still computed.
+ * Flagged and not computed (outputs unspecified): a request with more than
+ * max_tree_tokens drafted tokens (PKV_DEVERR_TREE), a malformed qo_indptr
+ * pair or more drafted tokens than keys (PKV_DEVERR_INDPTR), a seq_len outside
+ * the row (PKV_DEVERR_SEQ_LEN_RANGE), a negative table_idx. A parent that is
+ * not -1 or an earlier token counts as -1 (PKV_DEVERR_TREE). A key on a bad
+ * page reads as zeros (PKV_DEVERR_PAGE_RANGE). Rows of o and lse that belong
+ * to no request are left as they were. K/V rows of pages of 8 and more tokens
+ * (a multiple of 8) are read by TMA, others by 16-byte copies.
+ */
+pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *q,
+                               const int32_t *qo_indptr, const int32_t *parents, void *o,
+                               float *lse, const int32_t *page_table, int64_t table_stride,
+                               const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
+                               int32_t total_q, int32_t num_q_heads, float scale,
+                               int32_t max_tree_tokens, int32_t max_seq_len_hint, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Bytes of device workspace pkv_paged_cascade_decode_attn needs: fp32 partial

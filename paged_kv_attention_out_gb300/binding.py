@@ -89,6 +89,12 @@ def load() -> ctypes.CDLL:
                                               _p, _c_int64, _p, _p, _c_int32, _c_int32,
                                               _c_int32, ctypes.c_float, _c_int32, _c_int64, _p,
                                               ctypes.c_size_t, _p]
+    L.pkv_tree_workspace_size.restype = ctypes.c_size_t
+    L.pkv_tree_workspace_size.argtypes = [_c_int32] * 6
+    L.pkv_paged_tree_attn.restype = ctypes.c_int
+    L.pkv_paged_tree_attn.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _p, _p, _c_int64, _p, _p,
+                                      _c_int32, _c_int32, _c_int32, ctypes.c_float, _c_int32,
+                                      _c_int32, _p, ctypes.c_size_t, _p]
     L.pkv_cascade_workspace_size.restype = ctypes.c_size_t
     L.pkv_cascade_workspace_size.argtypes = [_c_int32] * 7
     L.pkv_paged_cascade_decode_attn.restype = ctypes.c_int
@@ -150,6 +156,43 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     if s2 != 1 or (s1 != d and h != 1):
         raise ValueError(f"{name} must have its heads and dims contiguous")
     return s0 if t.shape[0] != 1 else h * d
+
+
+def _queries(ps: PkvPool, q, o, lse) -> None:
+    """q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None) of the attention calls."""
+    for t, name in ((q, "q"), (o, "o")):
+        _want(t, torch.bfloat16, name, 3)
+        _contig(t, name)
+    if o.shape != q.shape or q.shape[2] != ps.head_dim:
+        raise ValueError("o must match q, with the pool's head_dim")
+    if lse is not None:
+        _want(lse, torch.float32, "lse", 2)
+        _contig(lse, "lse")
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [T, Hq]")
+
+
+def _tables(page_table, seq_lens, table_idx, batch: int) -> None:
+    """page_table [rows, stride], seq_lens [B] and table_idx [B] (or None), int32."""
+    _want(page_table, torch.int32, "page_table", 2)
+    _contig(page_table, "page_table")
+    _want(seq_lens, torch.int32, "seq_lens", 1)
+    _contig(seq_lens, "seq_lens")
+    if table_idx is not None:
+        _want(table_idx, torch.int32, "table_idx", 1)
+        _contig(table_idx, "table_idx")
+        if table_idx.shape[0] != batch:
+            raise ValueError("table_idx must have batch entries")
+    elif page_table.shape[0] < batch:
+        raise ValueError("page_table must have a row per request")
+
+
+def _workspace(workspace):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    _contig(workspace, "workspace")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pool_struct(pool: torch.Tensor) -> PkvPool:
@@ -411,6 +454,36 @@ def pkv_paged_extend_attn_store(pool, layer: int, q, k_new, v_new, qo_indptr, o,
         _ptr(qo_indptr), _ptr(o), _ptr(lse), _ptr(page_table), page_table.shape[1],
         _ptr(table_idx), _ptr(seq_lens), B, T, Hq, float(scale), int(max_seq_len_hint),
         int(max_total_keys_hint), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def pkv_tree_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                            max_tree_tokens: int, max_seq_len_hint: int) -> int:
+    return int(load().pkv_tree_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                              max_tree_tokens, max_seq_len_hint))
+
+
+def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_table, seq_lens,
+                        scale: float, max_tree_tokens: int, max_seq_len_hint: int,
+                        workspace=None, table_idx=None, stream=None) -> None:
+    """Attention of drafted tokens: q, o [T, Hq, D] bf16, qo_indptr [B+1] and parents [T] int32
+    (index within the request, -1 for a root); lse [T, Hq] fp32 or None; seq_lens count the
+    drafted tokens, whose keys are in the pool."""
+    ps = pool_struct(pool)
+    T, Hq, D = q.shape
+    B = seq_lens.shape[0]
+    _queries(ps, q, o, lse)
+    _tables(page_table, seq_lens, table_idx, B)
+    for t, name, n in ((qo_indptr, "qo_indptr", B + 1), (parents, "parents", T)):
+        _want(t, torch.int32, name, 1)
+        _contig(t, name)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} entries")
+    ws, ws_bytes = _workspace(workspace)
+    _one_device(pool, q, o, lse, qo_indptr, parents, page_table, seq_lens, table_idx, workspace)
+    _check(load().pkv_paged_tree_attn(
+        ctypes.byref(ps), int(layer), _ptr(q), _ptr(qo_indptr), _ptr(parents), _ptr(o), _ptr(lse),
+        _ptr(page_table), page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, T, Hq,
+        float(scale), int(max_tree_tokens), int(max_seq_len_hint), ws, ws_bytes, _stream(stream)))
 
 
 def pkv_cascade_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -47,16 +47,15 @@
 //              is refilled once every MMA that reads it is done.
 // Every hand-off is an mbarrier; every wait is bounded (tc_common.cuh).
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "tc_common.cuh"
+#include "tensor_map.h"
 
 namespace pkv {
 namespace {
@@ -1032,50 +1031,6 @@ int gather_ctas_per_sm() {
   return n;
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once per process.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// q [total_q][Hq][D] bf16 as a 3-D tensor, box {64, g, tpt}, 128-byte
-// swizzle; zeros outside.
-bool q3_map_of(CUtensorMap *m, const void *q, uint64_t total_q, uint64_t hq, uint64_t d,
-               uint32_t g, uint32_t tpt) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {d, hq, total_q};
-  cuuint64_t strides[2] = {d * 2, hq * d * 2};
-  cuuint32_t box[3] = {64, g, tpt};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A 2-D bf16 tensor of `rows` rows of `cols` elements (row-major), read in
-// boxes of box_rows rows x 64 columns with 128-byte swizzle; zeros outside.
-bool bf16_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 ExtendLayout extend_layout(int32_t batch, int32_t hkv, int32_t d, int64_t max_seq,
@@ -1153,8 +1108,8 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
   a.err = err;
   a.plan = ga.plan;
   CUtensorMap kv_map, q_map;
-  if (!bf16_map(&kv_map, workspace, ws_rows, static_cast<uint64_t>(g.d), kN) ||
-      !q3_map_of(&q_map, q, static_cast<uint64_t>(total_q), static_cast<uint64_t>(hq),
+  if (!tensor_map_rows(&kv_map, workspace, ws_rows, static_cast<uint64_t>(g.d), kN) ||
+      !tensor_map_q(&q_map, q, static_cast<uint64_t>(total_q), static_cast<uint64_t>(hq),
                  static_cast<uint64_t>(g.d), static_cast<uint32_t>(a.group),
                  static_cast<uint32_t>(a.tokens_per_tile)))
     return cudaErrorInvalidValue;

@@ -559,6 +559,82 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
                      max_total_keys_hint, workspace, workspace_bytes, stream);
 }
 
+size_t pkv_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t max_tree_tokens,
+                               int32_t max_seq_len_hint) {
+  if (batch <= 0 || batch > 65535 || num_kv_heads <= 0 || num_q_heads <= 0 ||
+      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > 16 ||
+      (head_dim != 64 && head_dim != 128) || max_tree_tokens < 1 ||
+      max_tree_tokens > PKV_MAX_TREE_TOKENS || max_seq_len_hint < 1)
+    return 0;
+  DevInfo *d = nullptr;
+  if (device_info(&d) != PKV_OK) return 0;
+  return pkv::tree_plan(batch, num_q_heads, num_kv_heads, head_dim, max_tree_tokens,
+                        max_seq_len_hint, d->sm_count)
+      .workspace_bytes;
+}
+
+pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *q,
+                               const int32_t *qo_indptr, const int32_t *parents, void *o,
+                               float *lse, const int32_t *page_table, int64_t table_stride,
+                               const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
+                               int32_t total_q, int32_t num_q_heads, float scale,
+                               int32_t max_tree_tokens, int32_t max_seq_len_hint, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  pkv::PoolGeom g;
+  pkv_status s = check_pool(pool, layer, &g);
+  if (s != PKV_OK) return s;
+  if (batch < 0 || total_q < 0) return fail(PKV_ERR_INVALID_ARG, "batch and total_q must be >= 0");
+  if (num_q_heads <= 0 || num_q_heads % g.hkv != 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of Hkv %d",
+                num_q_heads, g.hkv);
+  if (num_q_heads / g.hkv > 16)
+    return fail(PKV_ERR_UNSUPPORTED, "tree attention supports Hq/Hkv <= 16, got %d",
+                num_q_heads / g.hkv);
+  if (max_tree_tokens < 1) return fail(PKV_ERR_INVALID_ARG, "max_tree_tokens must be >= 1");
+  if (max_tree_tokens > PKV_MAX_TREE_TOKENS)
+    return fail(PKV_ERR_UNSUPPORTED, "max_tree_tokens %d > %d", max_tree_tokens,
+                PKV_MAX_TREE_TOKENS);
+  if (batch > 65535) return fail(PKV_ERR_UNSUPPORTED, "tree attention batch %d > 65535", batch);
+  if (g.hkv > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many kv heads");
+  if (table_stride <= 0) return fail(PKV_ERR_INVALID_ARG, "table_stride must be positive");
+  if (!isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (batch == 0 || total_q == 0) return PKV_OK;
+  if (!q || !o || !qo_indptr || !parents || !page_table || !seq_lens)
+    return fail(PKV_ERR_INVALID_ARG,
+                "q, o, qo_indptr, parents, page_table and seq_lens must be non-NULL");
+  if (!aligned(q, 16) || !aligned(o, 16))
+    return fail(PKV_ERR_INVALID_ARG, "q and o must be 16-byte aligned");
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+      !aligned(table_idx, 4) || !aligned(qo_indptr, 4) || !aligned(parents, 4))
+    return fail(PKV_ERR_INVALID_ARG, "int32/fp32 tables must be 4-byte aligned");
+  const int64_t row_capacity = table_stride * g.page_size;
+  if (row_capacity > 0x7fffff00)
+    return fail(PKV_ERR_UNSUPPORTED, "page-table rows of %lld keys (at most 2^31 - 256)",
+                static_cast<long long>(row_capacity));
+  int64_t cap = max_seq_len_hint >= 1 ? max_seq_len_hint : row_capacity;
+  if (cap > row_capacity) cap = row_capacity;
+  DevInfo *d = nullptr;
+  if ((s = device_info(&d)) != PKV_OK) return s;
+  const pkv::TreePlan plan =
+      pkv::tree_plan(batch, num_q_heads, g.hkv, g.d, max_tree_tokens, static_cast<int32_t>(cap),
+                     d->sm_count);
+  if (plan.workspace_bytes > 0) {
+    if (!workspace)
+      return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace is NULL, %zu bytes needed",
+                  plan.workspace_bytes);
+    if (workspace_bytes < plan.workspace_bytes)
+      return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", workspace_bytes,
+                  plan.workspace_bytes);
+    if (!aligned(workspace, 256))
+      return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  cudaError_t e = pkv::launch_tree(g, layer, q, qo_indptr, parents, o, lse, page_table,
+                                   table_stride, table_idx, seq_lens, batch, total_q, num_q_heads,
+                                   scale, max_tree_tokens, plan, workspace, d->err, stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "tree launch");
+}
+
 pkv_status pkv_merge_lse(const float *o_a, const float *lse_a, const float *o_b,
                          const float *lse_b, void *o_out, int32_t o_out_is_bf16,
                          float *lse_out, int64_t rows, int32_t heads, int32_t head_dim,

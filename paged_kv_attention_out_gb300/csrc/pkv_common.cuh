@@ -21,6 +21,7 @@ constexpr unsigned kErrSeqLen = 0x4;
 constexpr unsigned kErrIndptr = 0x8;
 constexpr unsigned kErrTableIdx = 0x10;
 constexpr unsigned kErrPosition = 0x40;
+constexpr unsigned kErrTree = 0x80;
 
 __device__ __forceinline__ void flag_error(unsigned *err, unsigned bit) {
   if (err) atomicOr(err, bit);

@@ -143,6 +143,26 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
                           void *workspace, int32_t sm_count, unsigned *err, cudaStream_t stream,
                           const ExtendMode &mode = ExtendMode());
 
+// Draft-tree attention (tree.cu): query tiles per block, query blocks per
+// request, groups the work is cut for, and the workspace (0 bytes for one
+// group), all from host scalars.
+struct TreePlan {
+  int32_t query_tiles;
+  int32_t blocks_per_req;
+  int32_t groups;
+  size_t lse_offset;
+  size_t table_offset;
+  size_t workspace_bytes;
+};
+TreePlan tree_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_tree,
+                   int32_t max_seq, int32_t sm_count);
+cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const int32_t *qo_indptr,
+                        const int32_t *parents, void *o, float *lse, const int32_t *page_table,
+                        int64_t table_stride, const int32_t *table_idx, const int32_t *seq_lens,
+                        int32_t batch, int32_t total_q, int32_t hq, float scale, int32_t max_tree,
+                        const TreePlan &plan, void *workspace, unsigned *err,
+                        cudaStream_t stream);
+
 cudaError_t launch_merge(const float *o_a, const float *lse_a, const float *o_b,
                          const float *lse_b, void *o_out, bool out_bf16, float *lse_out,
                          int64_t rows, int32_t heads, int32_t head_dim, int32_t sm_count,
