@@ -213,6 +213,45 @@ pkv_status pkv_paged_decode_attn_store(const pkv_pool *pool, int32_t layer, cons
                                        int32_t max_seq_len_hint, void *workspace,
                                        size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * What a model does to its attention scores between scale * q.k and the
+ * softmax, and which keys a query sees. With t the query's position in its
+ * row, i a key's, h the q head, in this order:
+ *   s = scale * q.k
+ *   s = soft_cap * tanh(s / soft_cap)            if soft_cap > 0
+ *   s = s - alibi_slopes[h] * |t - i|            if alibi_slopes
+ *   i is seen if i < prefix_lens[r], or if i <= t and (window = 0 or
+ *   t - i < window)
+ * so prefix_lens is a bidirectional prompt prefix (its queries see keys behind
+ * them) and, beside a window, the first keys that stay visible. All zero: the
+ * plain causal rule.
+ */
+typedef struct {
+  float soft_cap;              /* >= 0; 0: none                                */
+  const float *alibi_slopes;   /* device fp32 [num_q_heads], or NULL           */
+  int32_t window;              /* >= 0; 0: none                                */
+  const int32_t *prefix_lens;  /* device int32 [batch], clipped to 0 .. seq_len, or NULL */
+} pkv_score_mod;
+
+/*
+ * Decode attention under score rules: as pkv_paged_decode_attn for the keys
+ * that the rules let the newest position (t = seq_lens[b] - 1) see, their
+ * scores changed as above; mod NULL: none. Keys outside the rules are not
+ * read, nor are their page_table entries (their pages may have been freed).
+ * max_keys_hint: a bound on the keys a request sees, min(seq_len, window +
+ * prefix) with a window; it sets the split plan as max_seq_len_hint does, and
+ * the workspace is pkv_decode_workspace_size(batch, Hq, Hkv, D,
+ * max_keys_hint) bytes. A key on a bad page reads as zeros
+ * (PKV_DEVERR_PAGE_RANGE).
+ */
+pkv_status pkv_paged_decode_attn_mod(const pkv_pool *pool, int32_t layer, const void *q, void *o,
+                                     float *lse, const int32_t *page_table, int64_t table_stride,
+                                     const int32_t *table_idx, const int32_t *seq_lens,
+                                     int32_t batch, int32_t num_q_heads, float scale,
+                                     const pkv_score_mod *mod, int32_t max_keys_hint,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
 /* Size of the library-owned scratch used by pkv_paged_decode_attn_noalloc. */
 #define PKV_NOALLOC_SCRATCH_BYTES (32u << 20)
 
@@ -326,6 +365,24 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
                                        int32_t max_seq_len_hint, int64_t max_total_keys_hint,
                                        void *workspace, size_t workspace_bytes,
                                        cudaStream_t stream);
+
+/*
+ * Extend attention under score rules (pkv_score_mod): as pkv_paged_extend_attn
+ * with chunk query j of request r at position t = p_r + j; mod NULL: none. A
+ * prefix that reaches past the chunk ends with the request's keys (seq_lens[r]).
+ * Keys that no query of the request's chunk sees are not read, nor are their
+ * page_table entries. Hints, workspace and refusals as for
+ * pkv_paged_extend_attn (the workspace still has room for every key).
+ */
+pkv_status pkv_paged_extend_attn_mod(const pkv_pool *pool, int32_t layer, const void *q,
+                                     const int32_t *qo_indptr, void *o, float *lse,
+                                     const int32_t *page_table, int64_t table_stride,
+                                     const int32_t *table_idx, const int32_t *seq_lens,
+                                     int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                     float scale, const pkv_score_mod *mod,
+                                     int32_t max_seq_len_hint, int64_t max_total_keys_hint,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
 
 /* Most drafted tokens a request may have in pkv_paged_tree_attn. */
 #define PKV_MAX_TREE_TOKENS 256

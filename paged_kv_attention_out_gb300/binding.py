@@ -25,6 +25,11 @@ class PkvPool(ctypes.Structure):
                 ("page_size", _c_int32), ("num_kv_heads", _c_int32), ("head_dim", _c_int32)]
 
 
+class PkvScoreMod(ctypes.Structure):
+    _fields_ = [("soft_cap", ctypes.c_float), ("alibi_slopes", _p), ("window", _c_int32),
+                ("prefix_lens", _p)]
+
+
 PKV_OK = 0
 STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_WORKSPACE_TOO_SMALL", 4: "PKV_ERR_CUDA"}
@@ -78,6 +83,15 @@ def load() -> ctypes.CDLL:
     L.pkv_paged_decode_attn_noalloc.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _c_int64, _p,
                                                 _p, _c_int32, _c_int32, ctypes.c_float,
                                                 _c_int32, _p]
+    mod_p = ctypes.POINTER(PkvScoreMod)
+    L.pkv_paged_decode_attn_mod.restype = ctypes.c_int
+    L.pkv_paged_decode_attn_mod.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _c_int64, _p, _p,
+                                            _c_int32, _c_int32, ctypes.c_float, mod_p, _c_int32,
+                                            _p, ctypes.c_size_t, _p]
+    L.pkv_paged_extend_attn_mod.restype = ctypes.c_int
+    L.pkv_paged_extend_attn_mod.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _p, _c_int64, _p,
+                                            _p, _c_int32, _c_int32, _c_int32, ctypes.c_float,
+                                            mod_p, _c_int32, _c_int64, _p, ctypes.c_size_t, _p]
     L.pkv_extend_workspace_size.restype = ctypes.c_size_t
     L.pkv_extend_workspace_size.argtypes = [_c_int32] * 4 + [_c_int64]
     L.pkv_paged_extend_attn.restype = ctypes.c_int
@@ -309,6 +323,43 @@ def pkv_paged_decode_attn(pool, layer: int, q, o, lse, page_table, seq_lens, sca
         int(max_seq_len_hint), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int) -> PkvScoreMod:
+    if alibi_slopes is not None:
+        _want(alibi_slopes, torch.float32, "alibi_slopes", 1)
+        _contig(alibi_slopes, "alibi_slopes")
+        if alibi_slopes.shape[0] != hq:
+            raise ValueError("alibi_slopes must have one entry per q head")
+    if prefix_lens is not None:
+        _want(prefix_lens, torch.int32, "prefix_lens", 1)
+        _contig(prefix_lens, "prefix_lens")
+        if prefix_lens.shape[0] != batch:
+            raise ValueError("prefix_lens must have batch entries")
+    return PkvScoreMod(float(soft_cap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens))
+
+
+def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens, scale: float,
+                              max_keys_hint: int, workspace=None, soft_cap: float = 0.0,
+                              alibi_slopes=None, window: int = 0, prefix_lens=None,
+                              table_idx=None, stream=None) -> None:
+    """Decode attention under score rules: a soft cap, alibi_slopes [Hq] fp32, a window, and
+    prefix_lens [B] int32 first keys that stay visible. max_keys_hint: a bound on the keys a
+    request sees (min(seq_len, window + prefix) with a window)."""
+    ps = pool_struct(pool)
+    B, Hq, _ = q.shape
+    _queries(ps, q, o, lse)
+    _tables(page_table, seq_lens, table_idx, B)
+    if seq_lens.shape[0] != B:
+        raise ValueError("seq_lens must have batch entries")
+    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq)
+    ws, ws_bytes = _workspace(workspace)
+    _one_device(pool, q, o, lse, page_table, seq_lens, table_idx, alibi_slopes, prefix_lens,
+                workspace)
+    _check(load().pkv_paged_decode_attn_mod(
+        ctypes.byref(ps), int(layer), _ptr(q), _ptr(o), _ptr(lse), _ptr(page_table),
+        page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, Hq, float(scale),
+        ctypes.byref(mod), int(max_keys_hint), ws, ws_bytes, _stream(stream)))
+
+
 def pkv_paged_decode_attn_store(pool, layer: int, q, k_new, v_new, o, lse, page_table, seq_lens,
                                 scale: float, max_seq_len_hint: int, workspace=None,
                                 table_idx=None, stream=None) -> None:
@@ -412,6 +463,34 @@ def pkv_paged_extend_attn(pool, layer: int, q, qo_indptr, o, lse, page_table, se
         _ptr(page_table), page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, T, Hq,
         float(scale), int(max_seq_len_hint), int(max_total_keys_hint), _ptr(workspace), ws_bytes,
         _stream(stream)))
+
+
+def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table, seq_lens,
+                              scale: float, max_seq_len_hint: int, workspace,
+                              soft_cap: float = 0.0, alibi_slopes=None, window: int = 0,
+                              prefix_lens=None, table_idx=None, stream=None,
+                              max_total_keys_hint: int = 0) -> None:
+    """Extend attention under score rules (as pkv_paged_decode_attn_mod's), chunk query j of
+    request r at position seq_lens[r] - c_r + j; prefix_lens also lets the queries inside the
+    prefix see the keys behind them."""
+    ps = pool_struct(pool)
+    T, Hq, _ = q.shape
+    B = seq_lens.shape[0]
+    _queries(ps, q, o, lse)
+    _tables(page_table, seq_lens, table_idx, B)
+    _want(qo_indptr, torch.int32, "qo_indptr", 1)
+    _contig(qo_indptr, "qo_indptr")
+    if qo_indptr.shape[0] != B + 1:
+        raise ValueError("qo_indptr must have batch+1 entries")
+    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq)
+    ws, ws_bytes = _workspace(workspace)
+    _one_device(pool, q, o, lse, qo_indptr, page_table, seq_lens, table_idx, alibi_slopes,
+                prefix_lens, workspace)
+    _check(load().pkv_paged_extend_attn_mod(
+        ctypes.byref(ps), int(layer), _ptr(q), _ptr(qo_indptr), _ptr(o), _ptr(lse),
+        _ptr(page_table), page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, T, Hq,
+        float(scale), ctypes.byref(mod), int(max_seq_len_hint), int(max_total_keys_hint), ws,
+        ws_bytes, _stream(stream)))
 
 
 def pkv_paged_extend_attn_store(pool, layer: int, q, k_new, v_new, qo_indptr, o, lse,

@@ -22,6 +22,9 @@
 //  * Warps sharing a head, then splits, are merged by log-sum-exp: in shared
 //    memory inside the CTA, and by a small second kernel across splits (the
 //    partial states sit in the caller's workspace and are mostly L2 hits).
+//  * Score rules (a soft cap, a bias linear in the distance, a window with an
+//    always visible prefix) are compile-time variants: the visible keys are
+//    walked as one run without a gap, so a window costs what its keys cost.
 //  * The split size comes from host scalars only (batch, heads, a bound on
 //    seq_len, SM count), so the call never syncs and is graph-capturable.
 #include <math.h>
@@ -42,8 +45,8 @@ namespace {
 #define PKV_MERGE_BATCH 16  // partial rows the merge loads in its first round trip
 #endif
 
-template <int D>
-__global__ void __launch_bounds__(kDecodeThreads, (kDecodeStages <= 3 ? 2 : 1)) decode_kernel(const DecodeArgs a) {
+template <int D, typename Args>
+__global__ void __launch_bounds__(kDecodeThreads, (kDecodeStages <= 3 ? 2 : 1)) decode_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   if (!a.defer_wait) grid_dependency_wait();  // inputs may come from the previous kernel (store_kv)
   grid_dependents_launch();  // the split merge may be scheduled as CTAs drain
@@ -66,11 +69,11 @@ constexpr int kMergeThreads = 128;
 #endif
 
 
-template <int D>
-__device__ __forceinline__ void merge_pair(const DecodeArgs &a, int64_t bh, int lane);
+template <int D, typename Args>
+__device__ __forceinline__ void merge_pair(const Args &a, int64_t bh, int lane);
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const DecodeArgs a, int32_t batch) {
+template <int D, typename Args>
+__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Args a, int32_t batch) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t pairs = static_cast<int64_t>(batch) * a.hq;
@@ -84,8 +87,8 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
   for (; bh < pairs; bh += stride) merge_pair<D>(a, bh, lane);
 }
 
-template <int D>
-__device__ __forceinline__ void merge_pair(const DecodeArgs &a, int64_t bh, int lane) {
+template <int D, typename Args>
+__device__ __forceinline__ void merge_pair(const Args &a, int64_t bh, int lane) {
   const int b = static_cast<int>(bh / a.hq);
   const RowInfo ri = row_info(a, b, false);
   const int n = ri.nsplit;
@@ -171,8 +174,8 @@ constexpr int kNarrowStates = 4;
 #define PKV_MERGE_NARROW 1  // 0: every merge through decode_merge_kernel
 #endif
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) decode_merge_narrow_kernel(const DecodeArgs a,
+template <int D, typename Args>
+__global__ void __launch_bounds__(kMergeThreads) decode_merge_narrow_kernel(const Args a,
                                                                            int32_t batch) {
   constexpr int kLanes = D / 16;       // lanes per (request, q head) pair
   constexpr int kPairs = 32 / kLanes;  // pairs per warp
@@ -324,42 +327,64 @@ static DecodeArgs decode_args(const PoolGeom &g, int32_t layer, const void *q, v
   return a;
 }
 
-static cudaError_t launch_decode_main(const DecodeArgs &a, const PoolGeom &g,
-                                      const DecodePlan &plan, int32_t batch, cudaStream_t stream) {
-  cudaError_t e;
-  const dim3 grid(plan.head_groups, plan.splits, batch);
-  if (g.d == 128) {
-    e = cudaFuncSetAttribute(decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             DecodeSmem<128>::kTotal);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(decode_kernel<128>, grid, dim3(kDecodeThreads), DecodeSmem<128>::kTotal, stream, a);
-  } else {
-    e = cudaFuncSetAttribute(decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             DecodeSmem<64>::kTotal);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(decode_kernel<64>, grid, dim3(kDecodeThreads), DecodeSmem<64>::kTotal, stream, a);
-  }
-  return e;
+template <int D, typename Args>
+static cudaError_t launch_decode_main_d(const Args &a, dim3 grid, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, Args>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DecodeSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_kernel<D, Args>, grid, dim3(kDecodeThreads), DecodeSmem<D>::kTotal,
+                    stream, a);
 }
 
-static cudaError_t launch_decode_merge(const DecodeArgs &a, const PoolGeom &g, int32_t batch,
+template <typename Args>
+static cudaError_t launch_decode_main(const Args &a, const PoolGeom &g, const DecodePlan &plan,
+                                      int32_t batch, cudaStream_t stream) {
+  const dim3 grid(plan.head_groups, plan.splits, batch);
+  return g.d == 128 ? launch_decode_main_d<128>(a, grid, stream)
+                    : launch_decode_main_d<64>(a, grid, stream);
+}
+
+template <typename Args>
+static cudaError_t launch_decode_merge(const Args &a, const PoolGeom &g, int32_t batch,
                                        int32_t sm_count, cudaStream_t stream) {
   const int64_t pairs = static_cast<int64_t>(batch) * a.hq;
   if (PKV_MERGE_NARROW && a.pstride <= kNarrowStates) {
     const int64_t per_cta = (kMergeThreads / 32) * (32 / (g.d / 16));
     const dim3 ngrid(static_cast<unsigned>((pairs + per_cta - 1) / per_cta));
     if (g.d == 128)
-      return launch_pdl(decode_merge_narrow_kernel<128>, ngrid, dim3(kMergeThreads), 0, stream, a,
-                        batch);
-    return launch_pdl(decode_merge_narrow_kernel<64>, ngrid, dim3(kMergeThreads), 0, stream, a,
-                      batch);
+      return launch_pdl(decode_merge_narrow_kernel<128, Args>, ngrid, dim3(kMergeThreads), 0,
+                        stream, a, batch);
+    return launch_pdl(decode_merge_narrow_kernel<64, Args>, ngrid, dim3(kMergeThreads), 0, stream,
+                      a, batch);
   }
   int64_t ctas = (pairs + 3) / 4;
   const int64_t wave = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * PKV_MERGE_CTAS_PER_SM;
   if (ctas > wave) ctas = wave;
   const dim3 mgrid(static_cast<unsigned>(ctas));
-  if (g.d == 128) return launch_pdl(decode_merge_kernel<128>, mgrid, dim3(128), 0, stream, a, batch);
-  return launch_pdl(decode_merge_kernel<64>, mgrid, dim3(128), 0, stream, a, batch);
+  if (g.d == 128)
+    return launch_pdl(decode_merge_kernel<128, Args>, mgrid, dim3(128), 0, stream, a, batch);
+  return launch_pdl(decode_merge_kernel<64, Args>, mgrid, dim3(128), 0, stream, a, batch);
+}
+
+// Decode with score rules: the main kernel compiled for the rules in use, the
+// merge for the ranges alone (it only has to find a request's splits).
+static cudaError_t launch_decode_rules(const DecodeArgs &base, const ScoreRules &rules,
+                                       const PoolGeom &g, const DecodePlan &plan, int32_t batch,
+                                       cudaStream_t stream) {
+  DecodeRuleArgs a{base, rules};
+  const bool cap = rules.cap_log2 > 0.f, bias = rules.alibi_slopes != nullptr;
+  cudaError_t e;
+  if (cap && bias)
+    e = launch_decode_main(DecodeRulesArgs<kRuleCap | kRuleBias>(a), g, plan, batch, stream);
+  else if (cap)
+    e = launch_decode_main(DecodeRulesArgs<kRuleCap>(a), g, plan, batch, stream);
+  else if (bias)
+    e = launch_decode_main(DecodeRulesArgs<kRuleBias>(a), g, plan, batch, stream);
+  else
+    e = launch_decode_main(DecodeRulesArgs<0>(a), g, plan, batch, stream);
+  if (e != cudaSuccess || plan.splits <= 1) return e;
+  return launch_decode_merge(DecodeRulesArgs<0>(a), g, batch, plan.sm_count, stream);
 }
 
 cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void *o, float *lse,
@@ -367,7 +392,7 @@ cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void 
                           const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
                           int32_t hq, float scale, const DecodePlan &plan, void *workspace,
                           unsigned *err, cudaStream_t stream, const void *k_new,
-                          const void *v_new, int64_t kv_row_stride) {
+                          const void *v_new, int64_t kv_row_stride, const ScoreRules *rules) {
   DecodeArgs a = decode_args(g, layer, q, o, lse, page_table, table_stride, table_idx, seq_lens,
                              hq, scale, plan, err);
   a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
@@ -381,6 +406,7 @@ cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void 
     a.part_o = static_cast<float *>(workspace);
     a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
   }
+  if (rules) return launch_decode_rules(a, *rules, g, plan, batch, stream);
   cudaError_t e = launch_decode_main(a, g, plan, batch, stream);
   if (e != cudaSuccess || plan.splits <= 1) return e;
   return launch_decode_merge(a, g, batch, plan.sm_count, stream);

@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include "pkv_common.cuh"
+#include "score_rules.cuh"
 
 namespace pkv {
 
@@ -40,6 +41,7 @@ struct DecodeSmem {
 };
 
 struct DecodeArgs {
+  static constexpr int kRules = 0;  // compile-time score rules (score_rules.cuh)
   const __nv_bfloat16 *pool;
   int64_t plane;
   int64_t slots;
@@ -81,6 +83,19 @@ struct DecodeArgs {
   int32_t defer_wait;
 };
 
+// The same with score rules. A request's visible keys (a prefix, then a window
+// up to the newest key) are taken as one run without a gap: key v of the run
+// is key v of the row below the prefix length, v + gap from there on, so no
+// key outside the rules is read and nothing is masked.
+struct DecodeRuleArgs : DecodeArgs {
+  ScoreRules rules;
+};
+template <int kBits>
+struct DecodeRulesArgs : DecodeRuleArgs {
+  static constexpr int kRules = kRuleRanges | kBits;
+  explicit DecodeRulesArgs(const DecodeRuleArgs &a) : DecodeRuleArgs(a) {}
+};
+
 __device__ __forceinline__ float decode_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -94,11 +109,13 @@ __device__ __forceinline__ uint32_t ld_b32(const __nv_bfloat16 *p) {
 // Request-level facts every CTA (and the merge kernel) derives the same way.
 struct RowInfo {
   const int32_t *row;
-  int seq;
+  int seq;  // keys to attend
   int nsplit;
+  int prefix, gap;  // score rules: key v of them is key v (< prefix) or v + gap of the row
 };
 
-__device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int b, bool report) {
+template <typename Args>
+__device__ __forceinline__ RowInfo row_info(const Args &a, int b, bool report) {
   RowInfo r;
   int row_id = a.table_idx ? a.table_idx[b] : b;
   int seq = a.seq_lens[b];
@@ -113,6 +130,15 @@ __device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int b, bool rep
     seq = seq < 0 ? 0 : static_cast<int>(max_keys);
   }
   r.row = a.page_table + static_cast<int64_t>(row_id) * a.table_stride;
+  r.prefix = seq;
+  r.gap = 0;
+  if constexpr (Args::kRules != 0) {
+    const int lo = a.rules.window > 0 ? max(0, seq - a.rules.window) : 0;
+    const int pre = a.rules.prefix_lens ? min(max(a.rules.prefix_lens[b], 0), lo) : 0;
+    r.prefix = pre;
+    r.gap = lo - pre;
+    seq -= r.gap;
+  }
   r.seq = seq;
   int n = (seq + a.chunk - 1) / a.chunk;
   r.nsplit = n < 1 ? 1 : (n > a.splits ? a.splits : n);
@@ -123,8 +149,8 @@ __device__ __forceinline__ RowInfo row_info(const DecodeArgs &a, int b, bool rep
 // of request b, computed by kDecodeThreads threads (tid 0 .. kDecodeThreads - 1, whole
 // warps) in `smem` (DecodeSmem<D, kSt>::kTotal bytes, 128-byte aligned);
 // sync() is a barrier over exactly those threads.
-template <int D, int kSt, typename Sync>
-__device__ __forceinline__ void decode_body(const DecodeArgs &a, int hg, int split, int b,
+template <int D, int kSt, typename Args, typename Sync>
+__device__ __forceinline__ void decode_body(const Args &a, int hg, int split, int b,
                                             int tid, uint8_t *smem, Sync sync) {
   using S = DecodeSmem<D, kSt>;
   constexpr int kStages = kSt;
@@ -182,6 +208,19 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, int hg, int spl
     }
   }
 
+  // key of the row at place v of the attended run
+  auto row_key = [&](int v) -> int {
+    if constexpr (Args::kRules != 0) return v < ri.prefix ? v : v + ri.gap;
+    return v;
+  };
+  float slope0 = 0.f, slope1 = 0.f;  // of this lane's two score columns, log2 units
+  if constexpr ((Args::kRules & kRuleBias) != 0) {
+    const int n = (lane & 3) * 2;
+    const float *sl = a.rules.alibi_slopes + kvh * a.group;
+    slope0 = n < a.group ? sl[n] * kLog2e : 0.f;
+    slope1 = n + 1 < a.group ? sl[n + 1] * kLog2e : 0.f;
+  }
+
   float acc[D / 16][4];
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -206,8 +245,9 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, int hg, int spl
   auto load_entry = [&](int j) -> int {
     int e = -1;
     if (lane < kDecodeTileKeys && j < my_tiles) {
-      const int key = key_begin + (sub + j * a.warps_per_head) * kDecodeTileKeys + lane;
-      if (key < key_end) e = __ldg(ri.row + ((P == 1) ? key : key / P));
+      const int place = key_begin + (sub + j * a.warps_per_head) * kDecodeTileKeys + lane;
+      const int key = row_key(place);
+      if (place < key_end) e = __ldg(ri.row + ((P == 1) ? key : key / P));
     }
     return e;
   };
@@ -215,7 +255,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, int hg, int spl
     const int k0 = key_begin + (sub + j * a.warps_per_head) * kDecodeTileKeys;
     long long slot = -1;
     if (lane < kDecodeTileKeys && k0 + lane < key_end) {
-      const int key = k0 + lane;
+      const int key = row_key(k0 + lane);
       const int off = (P == 1) ? 0 : key % P;
       const long long s = static_cast<long long>(entry) * P + off;
       if (entry < 0 || s >= a.slots) {
@@ -283,10 +323,27 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, int hg, int spl
     // s[0]: key r0, head n0; s[1]: key r0, head n0+1; s[2], s[3]: key r0 + 8.
     const bool ok0 = k0 + r0 < key_end;
     const bool ok1 = k0 + r0 + 8 < key_end;
-    s[0] = ok0 ? s[0] * a.scale_log2 : -INFINITY;
-    s[1] = ok0 ? s[1] * a.scale_log2 : -INFINITY;
-    s[2] = ok1 ? s[2] * a.scale_log2 : -INFINITY;
-    s[3] = ok1 ? s[3] * a.scale_log2 : -INFINITY;
+    if constexpr ((Args::kRules & kRuleCap) != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = a.rules.cap_log2 * rule_tanh(s[i] * a.rules.cap_in);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] *= a.scale_log2;
+    }
+    if constexpr ((Args::kRules & kRuleBias) != 0) {
+      // the query is the row's last key: distances are >= 0
+      const int last = ri.seq + ri.gap - 1;
+      const float d0 = static_cast<float>(last - row_key(k0 + r0));
+      const float d1 = static_cast<float>(last - row_key(k0 + r0 + 8));
+      s[0] -= slope0 * d0;
+      s[1] -= slope1 * d0;
+      s[2] -= slope0 * d1;
+      s[3] -= slope1 * d1;
+    }
+    s[0] = ok0 ? s[0] : -INFINITY;
+    s[1] = ok0 ? s[1] : -INFINITY;
+    s[2] = ok1 ? s[2] : -INFINITY;
+    s[3] = ok1 ? s[3] : -INFINITY;
     float mx0 = fmaxf(s[0], s[2]);
     float mx1 = fmaxf(s[1], s[3]);
 #pragma unroll

@@ -46,6 +46,12 @@
 //              keys x 64 columns, 128-byte swizzle) into two stages; a stage
 //              is refilled once every MMA that reads it is done.
 // Every hand-off is an mbarrier; every wait is bounded (tc_common.cuh).
+//
+// Score rules (a soft cap, a bias linear in the distance, a window, a prefix
+// that every query sees) are compile-time variants of both kernels: the gather
+// copies only rows that some query of the request sees, an item walks only the
+// key tiles that hold such rows (a run of prefix tiles, then the window's), and
+// the softmax warps transform the scores in registers before the row maximum.
 #include <cuda.h>
 #include <math.h>
 
@@ -54,6 +60,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "score_rules.cuh"
 #include "tc_common.cuh"
 #include "tensor_map.h"
 
@@ -121,9 +128,13 @@ struct GatherArgs {
   const __nv_bfloat16 *v_new;
   int64_t kv_row_stride;
   __nv_bfloat16 *pool_w;
+  // Score rules (kRules): which keys a request's queries see
+  int32_t window;
+  const int32_t *prefix_lens;
 };
 
 struct ExtendArgs {
+  static constexpr int kRules = 0;  // compile-time score rules (score_rules.cuh)
   const int32_t *qo_indptr;
   __nv_bfloat16 *o;
   float *lse;
@@ -146,6 +157,33 @@ struct ExtendArgs {
   unsigned *err;
   int32_t *plan;  // the persistent form takes its work items from plan[1]
 };
+
+struct ExtendRuleArgs : ExtendArgs {
+  ScoreRules rules;
+};
+template <int kBits>
+struct ExtendRulesArgs : ExtendRuleArgs {
+  static constexpr int kRules = kRuleRanges | kBits;
+  explicit ExtendRulesArgs(const ExtendRuleArgs &a) : ExtendRuleArgs(a) {}
+};
+
+// The key tiles of an item whose tokens are at positions t0 .. of a request,
+// in the order walked: tiles 0 .. pre - 1 hold the always visible prefix,
+// tile v >= pre of the walk is tile v + gap of the request.
+struct TileWalk {
+  int pre, gap;
+};
+__device__ __forceinline__ TileWalk tile_walk(int t0, int window, int prefix) {
+  const int first = window > 0 ? max(0, t0 - window + 1) / kN : 0;
+  TileWalk w;
+  w.pre = min((prefix + kN - 1) / kN, first);
+  w.gap = first - w.pre;
+  return w;
+}
+// The request's always visible keys, within its row.
+__device__ __forceinline__ int rule_prefix(const int32_t *prefix_lens, int r, int seq) {
+  return prefix_lens ? min(max(prefix_lens[r], 0), seq) : 0;
+}
 
 constexpr int kGatherKeys = 16;     // keys per chunk of a gather CTA (two per warp)
 constexpr int kGatherWaves = 2;     // copying CTAs: this many waves of resident CTAs
@@ -206,6 +244,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
   return v + before;
 }
 
+template <bool kRules>
 __device__ void plan_blocks(const GatherArgs &a) {
   __shared__ int s_first_bad;
   __shared__ int s_part[kGatherThreads];
@@ -271,8 +310,14 @@ __device__ void plan_blocks(const GatherArgs &a) {
       const int tokens = min(per, c - j0);
       const int tok0 = min(a.tokens_per_tile, tokens);
       const int tok1 = max(0, tokens - a.tokens_per_tile);
-      const int n0 = (p + j0 + tok0 + 127) / 128;
-      const int n1 = tok1 == 0 ? 0 : (p + j0 + a.tokens_per_tile + tok1 + 127) / 128;
+      int n0 = (p + j0 + tok0 + 127) / 128;
+      int n1 = tok1 == 0 ? 0 : (p + j0 + a.tokens_per_tile + tok1 + 127) / 128;
+      if (kRules) {
+        const int pre = rule_prefix(a.prefix_lens, r, p + c);
+        const int gap = tile_walk(p + j0, a.window, pre).gap;
+        n0 = max(n0, (pre + 127) / 128) - gap;
+        n1 = tok1 == 0 ? 0 : max(n1, (pre + 127) / 128) - gap;
+      }
       const int cost = min(n0 + n1 + 2, nbuck - 1);
       const int b = first + i;
       ent[3 * b] = r;
@@ -323,17 +368,19 @@ __device__ void plan_blocks(const GatherArgs &a) {
 
 // kStore: the fused store (a.k_new != nullptr), a separate instantiation so
 // the plain gather keeps its lean inner loop.
-template <int D, bool kStore>
+// kRules: rows outside every query's window and the prefix are not read (nor,
+// for key tiles without any other row, written).
+template <int D, bool kStore, bool kRules>
 __device__ __forceinline__ void gather_body(const GatherArgs &a);
-template <int D, bool kStore>
+template <int D, bool kStore, bool kRules>
 __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos);
 
-template <int D, bool kStore>
+template <int D, bool kStore, bool kRules>
 __global__ void __launch_bounds__(kGatherThreads)
     extend_gather_kernel(const GatherArgs a) {
   grid_dependency_wait();  // the chunk's K/V may come from the previous kernel (store_kv)
   grid_dependents_launch();
-  gather_body<D, kStore>(a);
+  gather_body<D, kStore, kRules>(a);
 }
 
 // Read-only 16-byte load / 16-byte store with an L2 eviction-priority
@@ -360,20 +407,20 @@ __device__ __forceinline__ uint64_t l2_evict_last_policy() {
 // The first CTA builds the schedule (dispatched before the copying CTAs);
 // the others copy 16-row chunks of the key space, chunk c by CTA 1 + c mod
 // (grid - 1), so a grid of whole waves finishes together.
-template <int D, bool kStore>
+template <int D, bool kStore, bool kRules>
 __device__ __forceinline__ void gather_body(const GatherArgs &a) {
   if (blockIdx.x == 0) {
-    plan_blocks(a);
+    plan_blocks<kRules>(a);
     return;
   }
   const int64_t chunks = a.cap_rows / kGatherKeys;
   for (int64_t c = blockIdx.x - 1; c < chunks; c += gridDim.x - 1)
-    if (!gather_rows<D, kStore>(a, c * kGatherKeys)) break;
+    if (!gather_rows<D, kStore, kRules>(a, c * kGatherKeys)) break;
 }
 
 // Copies rows pos .. pos + 15 of the key space. Returns false once pos lies
 // past every run (so does every later chunk).
-template <int D, bool kStore>
+template <int D, bool kStore, bool kRules>
 __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
   // The request whose run holds these 16 rows (runs are multiples of 128
   // rows, so they never straddle two requests): the same scan of the
@@ -421,6 +468,16 @@ __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
       new_row0 = static_cast<int64_t>(beg) - new_key0;
     }
   }
+  // Score rules: the keys below `pre` and from `lo` on are seen by a query.
+  int lo = 0, pre = 0;
+  if (kRules) {
+    const int beg = a.qo_indptr[r], end = a.qo_indptr[r + 1];
+    if (a.window > 0 && beg >= 0 && end >= beg && end <= a.total_q && end - beg <= seq)
+      lo = max(0, seq - (end - beg) - a.window + 1);
+    pre = rule_prefix(a.prefix_lens, r, seq);
+    const int tile0 = key0 / 128 * 128;
+    if (tile0 >= pre && tile0 + 128 <= lo) return true;  // a tile nobody walks
+  }
   // One warp per key: its K row and V row (Hkv * D contiguous elements each
   // in the pool); 16-byte chunk `ch` of a row goes to kv head ch / (D / 8)'s run.
   constexpr int kChunks = D / 8;  // 16-byte chunks per head row
@@ -438,7 +495,7 @@ __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
     // the key's K row (c = 0) and V row (c = 1) are copied together
     const uint4 *src[2] = {nullptr, nullptr};
     uint4 *store[2] = {nullptr, nullptr};  // fused store: the key's pool rows
-    if (key < seq) {
+    if (key < seq && (!kRules || key >= lo || key < pre)) {
       const int pidx = key / a.page_size;
       const int ent = __ldg(row_pages + pidx);
       const int64_t slot = static_cast<int64_t>(ent) * a.page_size + (key - pidx * a.page_size);
@@ -543,26 +600,42 @@ constexpr std::integral_constant<int, 1> kTile1{};
 struct ItemDesc {
   int req, kvh, j0, c, p, off, t_base;
 };
+struct RuleItemDesc : ItemDesc {
+  int prefix;  // score rules: keys that every query sees
+};
+template <typename Args>
+using ItemOf = std::conditional_t<Args::kRules != 0, RuleItemDesc, ItemDesc>;
 
 // The item's split into query tiles and key tiles: query tile X holds
 // tokens X tpt .. X tpt + tok_X - 1 of the item and walks key tiles
 // 0 .. n_X - 1 (n_1 = 0 when it holds no token).
 struct ItemGeom {
   int tokens, n0, n1, n_tiles;
+  TileWalk walk;  // score rules: tile j of the item is a tile further on from walk.pre
 };
 
-__device__ __forceinline__ ItemGeom item_geom(const ItemDesc &d, int tpt) {
+template <typename Args>
+__device__ __forceinline__ ItemGeom item_geom(const ItemOf<Args> &d, const Args &a) {
+  const int tpt = a.tokens_per_tile;
   ItemGeom g;
   g.tokens = min(kQTiles * tpt, d.c - d.j0);
   const int tok1 = max(0, min(tpt, g.tokens - tpt));
   const int tok0 = min(tpt, g.tokens);
   g.n0 = (d.p + d.j0 + tok0 + kN - 1) / kN;
   g.n1 = tok1 == 0 ? 0 : (d.p + d.j0 + tpt + tok1 + kN - 1) / kN;
+  if constexpr (Args::kRules != 0) {
+    g.walk = tile_walk(d.p + d.j0, a.rules.window, d.prefix);
+    g.n0 = max(g.n0, (d.prefix + kN - 1) / kN) - g.walk.gap;
+    if (tok1 > 0) g.n1 = max(g.n1, (d.prefix + kN - 1) / kN) - g.walk.gap;
+  }
   g.n_tiles = max(g.n0, g.n1);
   return g;
 }
 
-__device__ __forceinline__ ItemDesc shfl_desc(ItemDesc d) {
+template <typename Item>
+__device__ __forceinline__ Item shfl_desc(Item d) {
+  if constexpr (std::is_same_v<Item, RuleItemDesc>)
+    d.prefix = __shfl_sync(0xffffffffu, d.prefix, 0);
   d.req = __shfl_sync(0xffffffffu, d.req, 0);
   d.kvh = __shfl_sync(0xffffffffu, d.kvh, 0);
   d.j0 = __shfl_sync(0xffffffffu, d.j0, 0);
@@ -573,16 +646,83 @@ __device__ __forceinline__ ItemDesc shfl_desc(ItemDesc d) {
   return d;
 }
 
+// Capped scores in log2 units, in place: cap tanh(scale s / cap). Where every
+// score of the warp's rows is near zero against the cap, which the tile's
+// largest (mx*, from the loads) and smallest one tell, the polynomial runs on
+// the FMA pipe in pairs; the exponential form costs two more MUFU results per
+// score (ex2 and rcp beside the softmax's own ex2).
+__device__ __forceinline__ void cap_scores(float (&v)[kN], float mx0, float mx1, float mx2,
+                                           float mx3, const ScoreRules &rules) {
+  float lo = fminf(v[0], v[1]), lo1 = fminf(v[2], v[3]);
+#pragma unroll
+  for (int cc = 4; cc < kN; cc += 4) {
+    lo = min3f(lo, v[cc], v[cc + 1]);
+    lo1 = min3f(lo1, v[cc + 2], v[cc + 3]);
+  }
+  const float top = fmaxf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), -fminf(lo, lo1));
+  const bool far = !(top * rules.cap_in <= kTanhPoly);
+  if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+    for (int cc = 0; cc < kN; ++cc) v[cc] = rules.cap_log2 * rule_tanh(v[cc] * rules.cap_in);
+  } else {
+    // cap_log2 tanh(c s) = s (k1 + u (k3 + u (k5 + u (k7 + u k9)))), u = (c s)^2
+    const float k1 = rules.cap_log2 * rules.cap_in, k3 = k1 * kTanh3, k5 = k1 * kTanh5,
+                k7 = k1 * kTanh7, k9 = k1 * kTanh9;
+#pragma unroll
+    for (int cc = 0; cc < kN; cc += 2) {
+      const float2 s = make_float2(v[cc], v[cc + 1]);
+      const float2 x = __fmul2_rn(s, make_float2(rules.cap_in, rules.cap_in));
+      const float2 u = __fmul2_rn(x, x);
+      float2 p = __ffma2_rn(u, make_float2(k9, k9), make_float2(k7, k7));
+      p = __ffma2_rn(u, p, make_float2(k5, k5));
+      p = __ffma2_rn(u, p, make_float2(k3, k3));
+      p = __ffma2_rn(u, p, make_float2(k1, k1));
+      p = __fmul2_rn(s, p);
+      v[cc] = p.x;
+      v[cc + 1] = p.y;
+    }
+  }
+}
+
+// Scores in log2 units less slope times the distance, for the row whose query
+// is at column t of the tile (t < 0 or past its end for most). A row's
+// -slope t is the same for the whole tile: it is returned, not added, unless
+// the tile holds keys behind some row's query (ahead), whose distance is cc - t.
+template <bool kScaled>
+__device__ __forceinline__ float bias_scores(float (&v)[kN], float scale_log2, float slope, int t,
+                                             bool ahead) {
+  const float ft = static_cast<float>(t);
+  if (ahead) {
+#pragma unroll
+    for (int cc = 0; cc < kN; ++cc)
+      v[cc] = fmaf(-slope, fabsf(ft - cc), kScaled ? v[cc] : v[cc] * scale_log2);
+    return 0.f;
+  }
+#pragma unroll
+  for (int cc = 0; cc < kN; cc += 2) {
+    float2 x = make_float2(v[cc], v[cc + 1]);
+    if (!kScaled) x = __fmul2_rn(x, make_float2(scale_log2, scale_log2));
+    x = __ffma2_rn(make_float2(slope, slope), make_float2(cc, cc + 1), x);
+    v[cc] = x.x;
+    v[cc + 1] = x.y;
+  }
+  return -slope * ft;
+}
+
 // q3_map: q as a 3-D bf16 tensor [total_q][Hq][D], box {64, g, 128 / g}
 // (one query tile's half: its tokens x the g q heads of one kv head, rows in
 // (token, head) order as the tile's rows), 128-byte swizzle.
-template <int D>
+template <int D, typename Args>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_tc_persistent_kernel(const __grid_constant__ CUtensorMap kv_map,
-                                const __grid_constant__ CUtensorMap q3_map, const ExtendArgs a) {
+                                const __grid_constant__ CUtensorMap q3_map, const Args a) {
   using S = Smem<D>;
+  constexpr bool kRanges = (Args::kRules & kRuleRanges) != 0;
+  constexpr bool kCap = (Args::kRules & kRuleCap) != 0;
+  constexpr bool kBias = (Args::kRules & kRuleBias) != 0;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ItemDesc s_item[2];
+  using Item = ItemOf<Args>;
+  __shared__ Item s_item[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   // Per softmax warp: items taken, S tiles taken, items that used its query
@@ -660,7 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (k >= 2 &&
           !(ok = mbar_wait_warp(bar(kPBarItemEmpty + slot), ((k >> 1) - 1) & 1, abort)))
         break;
-      ItemDesc d{-1, 0, 0, 0, 0, 0, 0};
+      Item d{};
+      d.req = -1;
       if (lane == 0) {
         const int i = static_cast<int>(atomicAdd(counter, 1u));
         if (i < total_items) {
@@ -672,13 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           d.c = a.qo_indptr[d.req + 1] - d.t_base;
           d.p = a.seq_lens[d.req] - d.c;
           d.off = offs[d.req];
+          if constexpr (kRanges)
+            d.prefix = rule_prefix(a.rules.prefix_lens, d.req, a.seq_lens[d.req]);
         }
         s_item[slot] = d;
         mbar_arrive(bar(kPBarItemFull + slot));  // release: the slot's contents
       }
       d = shfl_desc(d);
       if (d.req < 0) break;
-      const ItemGeom ig = item_geom(d, tpt);
+      const ItemGeom ig = item_geom(d, a);
       if (k >= 1 && !(ok = mbar_wait_warp(bar(kPBarQEmpty), (k - 1) & 1, abort))) break;
       if (lane == 0) {
         // Query tile x: tokens t_base + j0 + x tpt .. + tpt - 1, the g q heads
@@ -707,12 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const uint32_t dst = sbase + S::kKV + st * 2 * S::kTileBytes;
           mbar_arrive_expect_tx(bar(kPBarFull + st), 2 * S::kTileBytes);
+          const int tile = kRanges && j >= ig.walk.pre ? j + ig.walk.gap : j;
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            tma_load_2d_hint(dst + h * (kN * 128), &kv_map, h * 64, k_run + j * kN,
+            tma_load_2d_hint(dst + h * (kN * 128), &kv_map, h * 64, k_run + tile * kN,
                              bar(kPBarFull + st), kv_policy);
             tma_load_2d_hint(dst + S::kTileBytes + h * (kN * 128), &kv_map, h * 64,
-                             v_run + j * kN, bar(kPBarFull + st), kv_policy);
+                             v_run + tile * kN, bar(kPBarFull + st), kv_policy);
           }
         }
         __syncwarp();
@@ -781,10 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int slot = k & 1;
         if (!(ok = mbar_wait_fast(bar(kPBarItemFull + slot), (k >> 1) & 1, abort))) break;
-        const ItemDesc d = s_item[slot];
+        const Item d = s_item[slot];
         mbar_arrive(bar(kPBarItemEmpty + slot));
         if (d.req < 0) break;
-        const ItemGeom ig = item_geom(d, tpt);
+        const ItemGeom ig = item_geom(d, a);
         const int n0 = ig.n0, n1 = ig.n1, n_tiles = ig.n_tiles;
         const uint32_t g0 = g;
         ok = mbar_wait_fast(bar(a.q_mode ? kPBarQReady : kPBarQFull), k & 1, abort) &&
@@ -839,11 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k = state[0];
       const int slot = k & 1;
       if (!(ok = mbar_wait_warp(bar(kPBarItemFull + slot), (k >> 1) & 1, abort))) break;
-      const ItemDesc d = s_item[slot];
+      const Item d = s_item[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kPBarItemEmpty + slot));
       if (d.req < 0) break;
-      const ItemGeom ig = item_geom(d, tpt);
+      const ItemGeom ig = item_geom(d, a);
       const int n_x = x == 0 ? ig.n0 : ig.n1;
       const int tok = x * tpt + tt;  // token within the item
       const int qtok = (tt < tpt && tok < ig.tokens) ? d.t_base + d.j0 + tok : -1;
@@ -851,6 +995,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last key of the tile's first token, and the last key this row may see
       const int min_limit = d.p + d.j0 + x * tpt;
       const int limit = min_limit + (valid ? tt : 0);
+      float slope = 0.f;  // of this row's head, log2 units per key
+      if constexpr (kBias)
+        slope = a.rules.alibi_slopes[d.kvh * a.group + r % a.group] * kLog2e;
       float m_used = -INFINITY, l = 0.f;
       if (a.q_mode != 0) {
         // Fold the softmax scale's sign into the item's Q (both query tiles,
@@ -888,10 +1035,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32_max(srow + 64, *reinterpret_cast<float(*)[32]>(&v[64]), mx2);
         tmem_ld32_max(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
         tmem_ld_wait();
-        const int key0 = j * kN;
-        if (key0 + kN - 1 > min_limit) {
+        const int key0 = (kRanges && j >= ig.walk.pre ? j + ig.walk.gap : j) * kN;
+        // Rules: from here v holds scores in log2 units, less row_add.
+        float row_add = 0.f;
+        if constexpr (kCap) cap_scores(v, mx0, mx1, mx2, mx3, a.rules);
+        if constexpr (kBias)
+          row_add = bias_scores<kCap>(v, a.scale_log2, slope, limit - key0,
+                                      key0 + kN - 1 > min_limit);
+        bool masked = key0 + kN - 1 > min_limit;
+        if constexpr (kRanges) {
+          // some row's window starts inside or behind the tile
+          const int window = a.rules.window;
+          if (window > 0 && key0 < min_limit + tpt - window) masked = true;
+          if (key0 + kN <= d.prefix) masked = false;
+        }
+        if (masked || kCap || kBias) {
+          if constexpr (kRanges) {
+            if (masked) {
+              // column cc is seen if lo <= cc <= hi or cc < pre
+              const int hi = limit - key0;
+              const int lo = a.rules.window > 0 ? hi - a.rules.window + 1 : -key0;
+              const int pre = d.prefix - key0;
 #pragma unroll
-          for (int cc = 0; cc < kN; ++cc) v[cc] = key0 + cc <= limit ? v[cc] : -INFINITY;
+              for (int cc = 0; cc < kN; ++cc)
+                v[cc] = (cc >= lo && cc <= hi) || cc < pre ? v[cc] : -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < kN; ++cc) v[cc] = key0 + cc <= limit ? v[cc] : -INFINITY;
+          }
           mx0 = fmaxf(v[0], v[1]);
           mx1 = fmaxf(v[2], v[3]);
           mx2 = fmaxf(v[4], v[5]);
@@ -904,7 +1076,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx3 = max3f(mx3, v[cc + 6], v[cc + 7]);
           }
         }
-        const float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
+        float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        if constexpr (!kCap && !kBias) mt *= a.scale_log2;
+        if constexpr (kBias) mt += row_add;
         // Lazy rescale: move the reference max only when a row's max grew by
         // more than 2^kRescaleThreshold (warp-uniform: tcgen05.ld/st are
         // .sync.aligned, so every lane takes part, with factor 1 where its
@@ -918,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m_new);
           m_used = m_new;
         }
-        const float nm = m_used == -INFINITY ? 0.f : -m_used;
+        const float nm = (m_used == -INFINITY ? 0.f : -m_used) + row_add;
         float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
 #pragma unroll
         for (int cc = 0; cc < kN; cc += 32) {
@@ -926,7 +1100,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float y0, y1;
-            fma2(y0, y1, v[cc + 2 * e], v[cc + 2 * e + 1], a.scale_log2, nm);
+            if constexpr (kCap || kBias) {
+              y0 = v[cc + 2 * e];
+              y1 = v[cc + 2 * e + 1];
+              add2(y0, y1, nm, nm);
+            } else {
+              fma2(y0, y1, v[cc + 2 * e], v[cc + 2 * e + 1], a.scale_log2, nm);
+            }
             y0 = fast_exp2(y0);
             y1 = fast_exp2(y1);
             if (e & 1)
@@ -1018,17 +1198,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Copying CTAs of one gather variant resident on an SM at once (looked up
 // once per variant).
-template <int D, bool kStore>
+template <int D, bool kStore, bool kRules>
 int gather_ctas_per_sm() {
   static const int n = [] {
     int b = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, extend_gather_kernel<D, kStore>,
-                                                         kGatherThreads, 0) == cudaSuccess &&
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+               &b, extend_gather_kernel<D, kStore, kRules>, kGatherThreads, 0) == cudaSuccess &&
                    b > 0
                ? b
                : 1;
   }();
   return n;
+}
+
+// The planner, then two waves of copying CTAs (twice as many as are resident
+// at once) looping over the 16-row chunks.
+template <int D, bool kStore, bool kRules>
+cudaError_t launch_gather(const GatherArgs &ga, int32_t sm_count, cudaStream_t stream) {
+  const int64_t chunks = ga.cap_rows / kGatherKeys;
+  const int64_t copiers = std::min<int64_t>(
+      chunks, static_cast<int64_t>(sm_count) * gather_ctas_per_sm<D, kStore, kRules>() *
+                  kGatherWaves);
+  return launch_pdl(extend_gather_kernel<D, kStore, kRules>,
+                    dim3(static_cast<unsigned>(1 + copiers)), dim3(kGatherThreads), 0, stream, ga);
+}
+
+template <int D, typename Args>
+cudaError_t launch_attention(const CUtensorMap &kv_map, const CUtensorMap &q_map, const Args &a,
+                             dim3 grid, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(extend_tc_persistent_kernel<D, Args>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Smem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(extend_tc_persistent_kernel<D, Args>, grid, dim3(kThreads), Smem<D>::kTotal,
+                    stream, kv_map, q_map, a);
+}
+
+template <int D>
+cudaError_t launch_extend_d(const GatherArgs &ga, const ExtendArgs &a, const ScoreRules *rules,
+                            const CUtensorMap &kv_map, const CUtensorMap &q_map, dim3 grid,
+                            int32_t sms, cudaStream_t stream) {
+  if (!rules) {
+    const cudaError_t e = ga.k_new ? launch_gather<D, true, false>(ga, sms, stream)
+                                   : launch_gather<D, false, false>(ga, sms, stream);
+    return e == cudaSuccess ? launch_attention<D>(kv_map, q_map, a, grid, stream) : e;
+  }
+  const cudaError_t e = launch_gather<D, false, true>(ga, sms, stream);
+  if (e != cudaSuccess) return e;
+  ExtendRuleArgs ra{a, *rules};
+  const bool cap = rules->cap_log2 > 0.f, bias = rules->alibi_slopes != nullptr;
+  if (cap && bias)
+    return launch_attention<D>(kv_map, q_map, ExtendRulesArgs<kRuleCap | kRuleBias>(ra), grid,
+                               stream);
+  if (cap) return launch_attention<D>(kv_map, q_map, ExtendRulesArgs<kRuleCap>(ra), grid, stream);
+  if (bias) return launch_attention<D>(kv_map, q_map, ExtendRulesArgs<kRuleBias>(ra), grid, stream);
+  return launch_attention<D>(kv_map, q_map, ExtendRulesArgs<0>(ra), grid, stream);
 }
 
 }  // namespace
@@ -1086,6 +1310,10 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
   ga.k_new = static_cast<const __nv_bfloat16 *>(mode.k_new);
   ga.v_new = static_cast<const __nv_bfloat16 *>(mode.v_new);
   ga.kv_row_stride = mode.kv_row_stride;
+  if (mode.rules) {
+    ga.window = mode.rules->window;
+    ga.prefix_lens = mode.rules->prefix_lens;
+  }
   ga.pool_w = static_cast<__nv_bfloat16 *>(const_cast<void *>(g.base));
   ga.plan = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + lay.plan_offset);
 
@@ -1116,42 +1344,12 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
   const int64_t per_cta = static_cast<int64_t>(kQTiles) * a.tokens_per_tile;
   const int64_t tiles = (static_cast<int64_t>(total_q) + per_cta - 1) / per_cta + batch;
   if (tiles > 65535 || batch >= 65535) return cudaErrorInvalidConfiguration;
-  // the planner, then two waves of copying CTAs (twice as many as are
-  // resident at once) looping over the 16-row chunks
-  const int64_t chunks = lay.cap_rows / kGatherKeys;
-  const int per_sm = g.d == 128 ? (ga.k_new ? gather_ctas_per_sm<128, true>() : gather_ctas_per_sm<128, false>())
-                                : (ga.k_new ? gather_ctas_per_sm<64, true>() : gather_ctas_per_sm<64, false>());
-  const int64_t copiers = std::min<int64_t>(
-      chunks, static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * per_sm * kGatherWaves);
-  const dim3 ggrid(static_cast<unsigned>(1 + copiers));
   // attention: one CTA per SM (whole-SM shared memory), at most one per work item
+  const int32_t sms = sm_count > 0 ? sm_count : 1;
   const int64_t items = static_cast<int64_t>(g.hkv) * tiles;
-  const dim3 pgrid(static_cast<unsigned>(std::min<int64_t>(sm_count > 0 ? sm_count : 1, items)));
-  cudaError_t e;
-  if (g.d == 128) {
-    e = ga.k_new ? launch_pdl(extend_gather_kernel<128, true>, ggrid, dim3(kGatherThreads), 0,
-                              stream, ga)
-                 : launch_pdl(extend_gather_kernel<128, false>, ggrid, dim3(kGatherThreads), 0,
-                              stream, ga);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(extend_tc_persistent_kernel<128>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<128>::kTotal);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(extend_tc_persistent_kernel<128>, pgrid, dim3(kThreads), Smem<128>::kTotal,
-                   stream, kv_map, q_map, a);
-  } else {
-    e = ga.k_new ? launch_pdl(extend_gather_kernel<64, true>, ggrid, dim3(kGatherThreads), 0,
-                              stream, ga)
-                 : launch_pdl(extend_gather_kernel<64, false>, ggrid, dim3(kGatherThreads), 0,
-                              stream, ga);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(extend_tc_persistent_kernel<64>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<64>::kTotal);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(extend_tc_persistent_kernel<64>, pgrid, dim3(kThreads), Smem<64>::kTotal,
-                   stream, kv_map, q_map, a);
-  }
-  return e;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sms, items)));
+  return g.d == 128 ? launch_extend_d<128>(ga, a, mode.rules, kv_map, q_map, grid, sms, stream)
+                    : launch_extend_d<64>(ga, a, mode.rules, kv_map, q_map, grid, sms, stream);
 }
 
 }  // namespace pkv

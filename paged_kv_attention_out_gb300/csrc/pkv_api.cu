@@ -11,6 +11,7 @@
 
 #include "pkv.h"
 #include "pkv_internal.h"
+#include "score_rules.cuh"
 
 namespace {
 
@@ -262,6 +263,33 @@ size_t pkv_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
       .workspace_bytes;
 }
 
+// The score rules of a call as the kernels take them; *used = false if they
+// change nothing.
+static pkv_status score_rules(const pkv_score_mod *mod, float scale, pkv::ScoreRules *out,
+                              bool *used) {
+  *used = false;
+  if (!mod) return PKV_OK;
+  if (!isfinite(mod->soft_cap) || mod->soft_cap < 0.f)
+    return fail(PKV_ERR_INVALID_ARG, "soft_cap must be finite and >= 0");
+  if (mod->window < 0) return fail(PKV_ERR_INVALID_ARG, "window must be >= 0");
+  if (!aligned(mod->alibi_slopes, 4) || !aligned(mod->prefix_lens, 4))
+    return fail(PKV_ERR_INVALID_ARG, "alibi_slopes and prefix_lens must be 4-byte aligned");
+  *out = pkv::ScoreRules{};
+  if (mod->soft_cap > 0.f) {
+    out->cap_in = scale / mod->soft_cap;
+    out->cap_log2 = mod->soft_cap * pkv::kLog2e;
+    // the kernels multiply a raw score by cap_in and by twice its log2(e)
+    if (!isfinite(out->cap_in * 4.f) || !isfinite(out->cap_log2) || out->cap_log2 < 1e-30f)
+      return fail(PKV_ERR_INVALID_ARG, "soft_cap %g out of range for scale %g",
+                  static_cast<double>(mod->soft_cap), static_cast<double>(scale));
+  }
+  out->alibi_slopes = mod->alibi_slopes;
+  out->window = mod->window;
+  out->prefix_lens = mod->prefix_lens;
+  *used = mod->soft_cap > 0.f || mod->alibi_slopes || mod->window > 0 || mod->prefix_lens;
+  return PKV_OK;
+}
+
 // Decode, optionally with the step's new key / value rows stored first
 // (k_new != NULL: the fused store of pkv_paged_decode_attn_store).
 static pkv_status decode_call(const pkv_pool *pool, int32_t layer, const void *q,
@@ -270,7 +298,8 @@ static pkv_status decode_call(const pkv_pool *pool, int32_t layer, const void *q
                               int64_t table_stride, const int32_t *table_idx,
                               const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
                               float scale, int32_t max_seq_len_hint, void *workspace,
-                              size_t workspace_bytes, cudaStream_t stream) {
+                              size_t workspace_bytes, cudaStream_t stream,
+                              const pkv_score_mod *mod = nullptr) {
   pkv::PoolGeom g;
   pkv_status s = check_pool(pool, layer, &g);
   if (s != PKV_OK) return s;
@@ -286,6 +315,9 @@ static pkv_status decode_call(const pkv_pool *pool, int32_t layer, const void *q
   if (batch > 65535) return fail(PKV_ERR_UNSUPPORTED, "decode batch %d > 65535", batch);
   if (table_stride <= 0) return fail(PKV_ERR_INVALID_ARG, "table_stride must be positive");
   if (!isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  pkv::ScoreRules rules;
+  bool ruled = false;
+  if ((s = score_rules(mod, scale, &rules, &ruled)) != PKV_OK) return s;
   if (batch == 0) return PKV_OK;
   if (!q || !o || !page_table || !seq_lens)
     return fail(PKV_ERR_INVALID_ARG, "q, o, page_table and seq_lens must be non-NULL");
@@ -310,7 +342,8 @@ static pkv_status decode_call(const pkv_pool *pool, int32_t layer, const void *q
   }
   cudaError_t e = pkv::launch_decode(g, layer, q, o, lse, page_table, table_stride, table_idx,
                                      seq_lens, batch, num_q_heads, scale, plan, workspace, d->err,
-                                     stream, k_new, v_new, kv_row_stride);
+                                     stream, k_new, v_new, kv_row_stride,
+                                     ruled ? &rules : nullptr);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "decode launch");
 }
 
@@ -323,6 +356,18 @@ pkv_status pkv_paged_decode_attn(const pkv_pool *pool, int32_t layer, const void
   return decode_call(pool, layer, q, nullptr, nullptr, 0, o, lse, page_table, table_stride,
                      table_idx, seq_lens, batch, num_q_heads, scale, max_seq_len_hint, workspace,
                      workspace_bytes, stream);
+}
+
+pkv_status pkv_paged_decode_attn_mod(const pkv_pool *pool, int32_t layer, const void *q, void *o,
+                                     float *lse, const int32_t *page_table, int64_t table_stride,
+                                     const int32_t *table_idx, const int32_t *seq_lens,
+                                     int32_t batch, int32_t num_q_heads, float scale,
+                                     const pkv_score_mod *mod, int32_t max_keys_hint,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  return decode_call(pool, layer, q, nullptr, nullptr, 0, o, lse, page_table, table_stride,
+                     table_idx, seq_lens, batch, num_q_heads, scale, max_keys_hint, workspace,
+                     workspace_bytes, stream, mod);
 }
 
 pkv_status pkv_paged_decode_attn_store(const pkv_pool *pool, int32_t layer, const void *q,
@@ -467,7 +512,8 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
                               const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
                               int32_t total_q, int32_t num_q_heads, float scale,
                               int32_t max_seq_len_hint, int64_t max_total_keys_hint,
-                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream,
+                              const pkv_score_mod *mod = nullptr) {
   pkv::PoolGeom g;
   pkv_status s = check_pool(pool, layer, &g);
   if (s != PKV_OK) return s;
@@ -481,6 +527,12 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
   if (g.hkv > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many kv heads");
   if (table_stride <= 0) return fail(PKV_ERR_INVALID_ARG, "table_stride must be positive");
   if (!isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  // the scale's sign is folded into Q, a zero scale zeroes it: the cap's
+  // factor is positive like the kernel's own
+  pkv::ScoreRules rules;
+  bool ruled = false;
+  if ((s = score_rules(mod, scale == 0.f ? 1.f : fabsf(scale), &rules, &ruled)) != PKV_OK)
+    return s;
   if (batch == 0 || total_q == 0) return PKV_OK;
   if (!q || !o || !qo_indptr || !page_table || !seq_lens)
     return fail(PKV_ERR_INVALID_ARG, "q, o, qo_indptr, page_table and seq_lens must be non-NULL");
@@ -515,6 +567,7 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
   mode.k_new = k_new;
   mode.v_new = v_new;
   mode.kv_row_stride = kv_row_stride;
+  mode.rules = ruled ? &rules : nullptr;
   cudaError_t e = pkv::launch_extend(g, layer, q, qo_indptr, o, lse, page_table, table_stride,
                                      table_idx, seq_lens, batch, total_q, num_q_heads, scale, lay,
                                      workspace, d->sm_count, d->err, stream, mode);
@@ -532,6 +585,21 @@ pkv_status pkv_paged_extend_attn(const pkv_pool *pool, int32_t layer, const void
   return extend_call(pool, layer, q, nullptr, nullptr, 0, qo_indptr, o, lse, page_table,
                      table_stride, table_idx, seq_lens, batch, total_q, num_q_heads, scale,
                      max_seq_len_hint, max_total_keys_hint, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_paged_extend_attn_mod(const pkv_pool *pool, int32_t layer, const void *q,
+                                     const int32_t *qo_indptr, void *o, float *lse,
+                                     const int32_t *page_table, int64_t table_stride,
+                                     const int32_t *table_idx, const int32_t *seq_lens,
+                                     int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                     float scale, const pkv_score_mod *mod,
+                                     int32_t max_seq_len_hint, int64_t max_total_keys_hint,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  return extend_call(pool, layer, q, nullptr, nullptr, 0, qo_indptr, o, lse, page_table,
+                     table_stride, table_idx, seq_lens, batch, total_q, num_q_heads, scale,
+                     max_seq_len_hint, max_total_keys_hint, workspace, workspace_bytes, stream,
+                     mod);
 }
 
 pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, const void *q,

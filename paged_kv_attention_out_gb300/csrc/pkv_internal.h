@@ -10,6 +10,8 @@
 
 namespace pkv {
 
+struct ScoreRules;  // score_rules.cuh
+
 // Pool geometry as the kernels use it.
 struct PoolGeom {
   const void *base;   // bf16 pool
@@ -74,7 +76,8 @@ cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void 
                           const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
                           int32_t hq, float scale, const DecodePlan &plan, void *workspace,
                           unsigned *err, cudaStream_t stream, const void *k_new = nullptr,
-                          const void *v_new = nullptr, int64_t kv_row_stride = 0);
+                          const void *v_new = nullptr, int64_t kv_row_stride = 0,
+                          const ScoreRules *rules = nullptr);
 
 // Cascade decode: the shared-prefix states of every member (cascade.cu,
 // slots splits .. splits + key ranges - 1 of [B, Hq, slots]), the suffix
@@ -116,6 +119,7 @@ struct ExtendMode {
   const void *k_new = nullptr;
   const void *v_new = nullptr;
   int64_t kv_row_stride = 0;
+  const ScoreRules *rules = nullptr;  // score rules (without a fused store)
 };
 
 // Workspace of the extend call, from host scalars only: the gathered K/V

@@ -350,6 +350,12 @@ __device__ __forceinline__ float max3f(float x, float y, float z) {
   return r;
 }
 
+__device__ __forceinline__ float min3f(float x, float y, float z) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // (y0, y1) = (x0, x1) * s + c, one packed fp32 instruction (the compiler's
 // own float2 builtin, so it pairs the registers and hoists the broadcasts).
 __device__ __forceinline__ void fma2(float &y0, float &y1, float x0, float x1, float s, float c) {

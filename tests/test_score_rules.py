@@ -1,0 +1,311 @@
+"""Decode and extend attention under score rules (pkv_paged_decode_attn_mod,
+pkv_paged_extend_attn_mod) against the definition in 64 bits (attn_reference.py derives the
+tolerances)."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from attn_reference import attend, check, stored_inputs
+from helpers import ensure_built, gpu_inputs, nan_outputs
+from paged_kv_attention_out_gb300 import workloads as W
+
+PAGE = 0x2
+
+
+class Rules:
+    """The rules of a call, as its keyword arguments and as the reference's functions."""
+
+    def __init__(self, case, cap=0.0, alibi=False, window=0, prefix=None):
+        self.case, self.cap, self.window = case, cap, window
+        self.slopes = 2.0 ** (-8.0 * np.arange(1, case.Hq + 1) / case.Hq) if alibi else None
+        if alibi:
+            self.slopes = self.slopes.astype(np.float32)
+        self.prefix = None if prefix is None else np.resize(np.asarray(prefix, np.int32), case.B)
+
+    def first(self, r):
+        """Position of request r's first query."""
+        n = int(self.case.seq_lens[r])
+        if self.case.kind == "decode":
+            return n - 1
+        return n - int(self.case.qo_indptr[r + 1] - self.case.qo_indptr[r])
+
+    def visible(self, r, j, n):
+        i, t = np.arange(n), self.first(r) + j
+        vis = i <= t
+        if self.window:
+            vis &= t - i < self.window
+        return vis if self.prefix is None else vis | (i < self.prefix[r])
+
+    def rule(self, s, r, j, h, idx):
+        if self.cap:
+            s = self.cap * np.tanh(s / self.cap)
+        if self.slopes is not None:
+            s = s - float(self.slopes[h]) * np.abs(self.first(r) + j - idx)
+        return s
+
+    def kwargs(self):
+        return dict(soft_cap=self.cap, window=self.window,
+                    alibi_slopes=None if self.slopes is None else torch.as_tensor(self.slopes).cuda(),
+                    prefix_lens=None if self.prefix is None else torch.as_tensor(self.prefix).cuda())
+
+    def max_keys(self):
+        """A bound on the keys a decode query sees."""
+        n = self.case.max_seq_len
+        if not self.window:
+            return n
+        return min(n, self.window + (0 if self.prefix is None else max(0, int(self.prefix.max()))))
+
+    def want(self, scale=None):
+        case = self.case
+        kv, q = stored_inputs(case)
+        qo = np.arange(case.B + 1) if case.kind == "decode" else case.qo_indptr
+        return attend(kv, q, qo, case.scale if scale is None else scale, self.visible, self.rule)
+
+
+def mod_run(rules, inputs=None, hint=None, scale=None, lse=True, before=None):
+    import paged_kv_attention_out_gb300 as pkv
+    case = rules.case
+    pool, k, v, q, t = inputs or gpu_inputs(case)
+    pkv.pkv_kv_store(pool, case.layer, k, v, t["out_loc"])
+    if before is not None:
+        before(pool, t)
+    o, l = nan_outputs(q, lse)
+    scale = case.scale if scale is None else scale
+    if case.kind == "decode":
+        h = rules.max_keys() if hint is None else hint
+        n = pkv.pkv_decode_workspace_size(case.B, case.Hq, case.Hkv, case.D, h)
+        ws = torch.full((max(n, 1),), 0xff, dtype=torch.uint8, device="cuda")
+        pkv.pkv_paged_decode_attn_mod(pool, case.layer, q, o, l, t["page_table"], t["seq_lens"],
+                                      scale, h, ws, table_idx=t.get("table_idx"), **rules.kwargs())
+    else:
+        h, total = case.max_seq_len, int(case.seq_lens.sum())
+        n = pkv.pkv_extend_workspace_size(case.B, case.Hkv, case.D, h, total)
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")  # NaN bits
+        pkv.pkv_paged_extend_attn_mod(pool, case.layer, q, t["qo_indptr"], o, l, t["page_table"],
+                                      t["seq_lens"], scale, h, ws, table_idx=t.get("table_idx"),
+                                      max_total_keys_hint=total, **rules.kwargs())
+    torch.cuda.synchronize()
+    return o, l
+
+
+def mod_check(rules, **kw):
+    import paged_kv_attention_out_gb300 as pkv
+    ensure_built()
+    pkv.pkv_read_device_errors()
+    o, lse = mod_run(rules, **kw)
+    assert pkv.pkv_read_device_errors() == 0
+    check(o, lse, rules.want(kw.get("scale")))
+    return o, lse
+
+
+RULES = [
+    dict(cap=30.0), dict(cap=2.0), dict(alibi=True), dict(window=100), dict(window=1),
+    dict(window=1000), dict(prefix=[40, 0, 700]), dict(window=64, prefix=[5, 0, 130, 300]),
+    dict(cap=1.0, alibi=True), dict(cap=50.0, window=200), dict(alibi=True, window=90, prefix=[17]),
+    dict(cap=20.0, alibi=True, window=129, prefix=[128, 1000]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", RULES, ids=str)
+@pytest.mark.parametrize("D,P,Hq,Hkv", [(64, 1, 8, 2), (128, 16, 32, 8), (128, 7, 7, 1)])
+def test_decode_rules(rule, D, P, Hq, Hkv):
+    case = W.random_case(3, seq_lens=[1, 40, 513, 900, 130, 64], Hq=Hq, Hkv=Hkv, D=D, P=P,
+                         use_table_idx=True)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", RULES, ids=str)
+@pytest.mark.parametrize("D,P,Hq,Hkv", [(64, 1, 4, 4), (128, 16, 8, 2), (128, 7, 7, 1)])
+def test_extend_rules(rule, D, P, Hq, Hkv):
+    case = W.random_case(4, kind="extend", seq_lens=[1, 160, 513, 260, 700],
+                         chunk_lens=[1, 160, 13, 129, 70], Hq=Hq, Hkv=Hkv, D=D, P=P,
+                         use_table_idx=True)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", [dict(window=300), dict(cap=25.0, window=2000, prefix=[700]),
+                                  dict(alibi=True)], ids=str)
+def test_long_rows(rule):
+    """Splits and their merge in decode, many key tiles behind a gap in extend."""
+    case = W.random_case(5, seq_lens=[9000, 300, 4097], Hq=8, Hkv=2, D=128, P=16)
+    mod_check(Rules(case, **rule))
+    case = W.random_case(6, kind="extend", seq_lens=[5000, 2049, 300], chunk_lens=[40, 129, 9],
+                         Hq=8, Hkv=2, D=128, P=16)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["decode", "extend"])
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+@pytest.mark.parametrize("rule", [dict(cap=3.0), dict(cap=3.0, alibi=True, window=50),
+                                  dict(alibi=True, prefix=[200])], ids=str)
+def test_negative_and_zero_scales(kind, scale, rule):
+    kw = dict(chunk_lens=[30, 64]) if kind == "extend" else {}
+    case = W.random_case(7, kind=kind, seq_lens=[150, 260], Hq=8, Hkv=2, D=64, P=16, **kw)
+    mod_check(Rules(case, **rule), scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["decode", "extend"])
+@pytest.mark.parametrize("cap", [1e-2, 0.5, 7.5, 1e4, 1e8])
+def test_caps_of_any_size(kind, cap):
+    """Caps that saturate every score, caps at the border of the two tanh forms, and caps far above
+    every score."""
+    kw = dict(chunk_lens=[30, 64]) if kind == "extend" else {}
+    case = W.random_case(8, kind=kind, seq_lens=[150, 400], Hq=8, Hkv=2, D=128, P=1, **kw)
+    mod_check(Rules(case, cap=cap))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["decode", "extend"])
+def test_no_rules_equal_the_plain_call_bitwise(kind):
+    import paged_kv_attention_out_gb300 as pkv
+    from helpers import gpu_attention
+    kw = dict(chunk_lens=[30, 300]) if kind == "extend" else {}
+    case = W.random_case(9, kind=kind, seq_lens=[1500, 400], Hq=8, Hkv=2, D=128, P=16, **kw)
+    inputs = gpu_inputs(case)
+    o, lse = mod_run(Rules(case), inputs=inputs)
+    o2, lse2 = gpu_attention(case, inputs[0], inputs[3], inputs[4])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # a window nobody reaches changes nothing but the kernel
+    check(*mod_run(Rules(case, window=100000), inputs=inputs), Rules(case).want())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["decode", "extend"])
+def test_pages_outside_the_rules_are_never_read(kind):
+    """Freed pages: table entries outside the window and prefix are garbage, their rows NaN."""
+    kw = dict(chunk_lens=[40, 130]) if kind == "extend" else {}
+    case = W.random_case(10, kind=kind, seq_lens=[900, 700], Hq=8, Hkv=2, D=64, P=16, **kw)
+    rules = Rules(case, window=100, prefix=[20, 0], cap=10.0)
+
+    def free(pool, t):
+        for r in range(case.B):
+            n = int(case.seq_lens[r])
+            first_seen = max(0, rules.first(r) - 99)
+            for pg in range(n // 16 + 1):
+                if pg * 16 >= rules.prefix[r] and pg * 16 + 16 <= first_seen:
+                    t["page_table"][r, pg] = -12345 - pg
+                    for off in range(16):
+                        s = int(case.token_slots[r][pg * 16 + off])
+                        pool[:, 0].flatten(1, 2)[:, s] = float("nan")
+                elif pg * 16 < first_seen:  # rows of a page in use, outside the rules
+                    for off in range(16):
+                        i = pg * 16 + off
+                        if rules.prefix[r] <= i < first_seen:
+                            s = int(case.token_slots[r][i])
+                            pool[:, 0].flatten(1, 2)[:, s] = float("nan")
+
+    mod_check(rules, before=free)
+
+
+@pytest.mark.gpu
+def test_empty_rows_and_prefix_clipping():
+    case = W.random_case(11, seq_lens=[4, 3, 50], Hq=8, Hkv=2, D=64, P=16)
+    rules = Rules(case, window=5, prefix=[7, -3, 1 << 30])
+
+    def empty(pool, t):
+        t["seq_lens"][0] = 0
+
+    o, lse = mod_run(rules, before=empty)
+    rules.prefix = np.array([0, 0, 50])
+    check(o, lse, rules.want(), rows=[1, 2])
+    assert not o[0].any() and torch.isneginf(lse[0]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hint", [0, 16, 5000])
+def test_decode_hint_changes_only_the_splits(hint):
+    case = W.random_case(12, seq_lens=[2000, 100], Hq=8, Hkv=2, D=64, P=16)
+    mod_check(Rules(case, window=700, cap=5.0), hint=hint)
+
+
+@pytest.mark.gpu
+def test_a_chunked_prompt_equals_the_whole():
+    """A prefix-LM prompt in one chunk, and its causal rest in two: the second chunk sees the
+    prefix that the first one stored."""
+    whole = W.random_case(13, kind="extend", seq_lens=[300], chunk_lens=[300], Hq=8, Hkv=2, D=128,
+                          P=16)
+    rules = Rules(whole, window=64, prefix=[90], cap=30.0)
+    o, lse = mod_check(rules)
+    import paged_kv_attention_out_gb300 as pkv
+    pool, k, v, q, t = gpu_inputs(whole)
+    pkv.pkv_kv_store(pool, 0, k, v, t["out_loc"])
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    parts = []
+    for a, b in ((0, 130), (130, 300)):
+        qo = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        n = torch.tensor([b], dtype=torch.int32, device="cuda")
+        po, pl = nan_outputs(q[a:b])
+        pkv.pkv_paged_extend_attn_mod(pool, 0, q[a:b].contiguous(), qo, po, pl, t["page_table"], n,
+                                      whole.scale, b, ws, **rules.kwargs())
+        parts.append((po, pl))
+    check(torch.cat([p[0] for p in parts]), torch.cat([p[1] for p in parts]), rules.want())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["decode", "extend"])
+def test_replay_in_a_graph_follows_new_lengths(kind):
+    import paged_kv_attention_out_gb300 as pkv
+    kw = dict(chunk_lens=[40, 130]) if kind == "extend" else {}
+    case = W.random_case(14, kind=kind, seq_lens=[900, 700], Hq=8, Hkv=2, D=128, P=16, **kw)
+    rules = Rules(case, cap=20.0, alibi=True, window=300, prefix=[10, 40])
+    pool, k, v, q, t = gpu_inputs(case)
+    pkv.pkv_kv_store(pool, 0, k, v, t["out_loc"])
+    o, lse = nan_outputs(q)
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    args = rules.kwargs()
+
+    def call():
+        if kind == "decode":
+            pkv.pkv_paged_decode_attn_mod(pool, 0, q, o, lse, t["page_table"], t["seq_lens"],
+                                          case.scale, 900, ws, **args)
+        else:
+            pkv.pkv_paged_extend_attn_mod(pool, 0, q, t["qo_indptr"], o, lse, t["page_table"],
+                                          t["seq_lens"], case.scale, 900, ws, **args)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    t["seq_lens"] -= 200
+    args["prefix_lens"] += 100
+    args["alibi_slopes"] *= 2
+    o.fill_(float("nan"))
+    g.replay()
+    first = o.clone(), lse.clone()
+    call()
+    assert torch.equal(first[0], o) and torch.equal(first[1], lse)
+    assert torch.isfinite(o.float()).all()
+
+
+def _decode(lib, pool, mod, hint=16):
+    return lib.pkv_paged_decode_attn_mod(ctypes.byref(pool), 0, 1 << 20, 1 << 20, None, 64, 8, None,
+                                         64, 1, 4, ctypes.c_float(0.125), ctypes.byref(mod), hint,
+                                         None, 0, None)
+
+
+def _extend(lib, pool, mod):
+    return lib.pkv_paged_extend_attn_mod(ctypes.byref(pool), 0, 1 << 20, 64, 1 << 20, None, 64, 8,
+                                         None, 64, 1, 4, 4, ctypes.c_float(0.125),
+                                         ctypes.byref(mod), 16, 0, None, 0, None)
+
+
+@pytest.mark.parametrize("mod", [(-1.0, None, 0, None), (float("inf"), None, 0, None),
+                                 (float("nan"), None, 0, None), (1e-39, None, 0, None),
+                                 (0.0, 2, 0, None), (0.0, None, -1, None), (0.0, None, 0, 6)])
+@pytest.mark.parametrize("call", [_decode, _extend])
+def test_refusals(call, mod):
+    ensure_built()
+    from paged_kv_attention_out_gb300 import binding
+    pool = binding.PkvPool(1 << 30, 1, 10, 16, 2, 64)
+    assert call(binding.load(), pool, binding.PkvScoreMod(*mod)) == 1
+    assert b"pool" not in binding.load().pkv_last_error()
