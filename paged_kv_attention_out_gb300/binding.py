@@ -136,8 +136,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building a Stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -155,56 +155,92 @@ def _contig(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _one_device(*tensors):
-    """Every tensor (None: skipped) lives on the current device, where the kernels run."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+# The calls below are launch-bound at decode sizes, so each tensor is checked by
+# one short expression; what is wrong is found out only when something is.
+def _refuse(t, dtype, ndim: int, dev: int, name: str):
+    _want(t, dtype, name, ndim)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    _contig(t, name)
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the rows of a [N, heads, D] tensor whose rows are contiguous."""
+def _arg(t, dtype, ndim: int, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of this type on the current device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != ndim \
+            or not t.is_contiguous():
+        _refuse(t, dtype, ndim, dev, name)
+    return t.data_ptr()
+
+
+def _rows_arg(t, shape, dev: int, name: str) -> tuple[int, int]:
+    """(address, elements between rows) of a bf16 [N, heads, D] tensor with contiguous rows."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
+        _want(t, torch.bfloat16, name, 3)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        _refuse(t, torch.bfloat16, 3, dev, name)
+    n, h, d = shape
     s0, s1, s2 = t.stride()
-    _, h, d = t.shape
     if s2 != 1 or (s1 != d and h != 1):
         raise ValueError(f"{name} must have its heads and dims contiguous")
-    return s0 if t.shape[0] != 1 else h * d
+    return t.data_ptr(), s0 if n != 1 else h * d
 
 
-def _queries(ps: PkvPool, q, o, lse) -> None:
-    """q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None) of the attention calls."""
-    for t, name in ((q, "q"), (o, "o")):
-        _want(t, torch.bfloat16, name, 3)
-        _contig(t, name)
-    if o.shape != q.shape or q.shape[2] != ps.head_dim:
-        raise ValueError("o must match q, with the pool's head_dim")
-    if lse is not None:
-        _want(lse, torch.float32, "lse", 2)
-        _contig(lse, "lse")
-        if lse.shape != q.shape[:2]:
-            raise ValueError("lse must be [T, Hq]")
+def _pool_arg(pool, dev: int) -> PkvPool:
+    base = _arg(pool, torch.bfloat16, 6, dev, "pool")
+    two, L, NP, P, H, D = pool.shape
+    if two != 2:
+        raise ValueError("pool dim 0 must be 2 (K, V)")
+    return PkvPool(base, L, NP, P, H, D)
 
 
-def _tables(page_table, seq_lens, table_idx, batch: int) -> None:
-    """page_table [rows, stride], seq_lens [B] and table_idx [B] (or None), int32."""
-    _want(page_table, torch.int32, "page_table", 2)
-    _contig(page_table, "page_table")
-    _want(seq_lens, torch.int32, "seq_lens", 1)
-    _contig(seq_lens, "seq_lens")
-    if table_idx is not None:
-        _want(table_idx, torch.int32, "table_idx", 1)
-        _contig(table_idx, "table_idx")
-        if table_idx.shape[0] != batch:
-            raise ValueError("table_idx must have batch entries")
-    elif page_table.shape[0] < batch:
-        raise ValueError("page_table must have a row per request")
+def _queries(q, o, lse, dev: int):
+    """Addresses of q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None)."""
+    shape = q.shape
+    qp = _arg(q, torch.bfloat16, 3, dev, "q")
+    op = _arg(o, torch.bfloat16, 3, dev, "o")
+    if o.shape != shape:
+        raise ValueError("o must match q")
+    if lse is None:
+        return qp, op, None
+    lp = _arg(lse, torch.float32, 2, dev, "lse")
+    if lse.shape != shape[:2]:
+        raise ValueError("lse must be [T, Hq]")
+    return qp, op, lp
 
 
-def _workspace(workspace):
-    """(pointer, bytes) of a workspace tensor or None."""
+def _tables(page_table, seq_lens, table_idx, batch: int, dev: int):
+    """Addresses of page_table [rows, stride], seq_lens [B], table_idx [B] (or None), and the
+    table's stride."""
+    pp = _arg(page_table, torch.int32, 2, dev, "page_table")
+    rows, stride = page_table.shape
+    sp = _arg(seq_lens, torch.int32, 1, dev, "seq_lens")
+    if seq_lens.shape[0] != batch:
+        raise ValueError("seq_lens must have batch entries")
+    if table_idx is None:
+        if rows < batch:
+            raise ValueError("page_table must have a row per request")
+        return pp, sp, None, stride
+    tp = _arg(table_idx, torch.int32, 1, dev, "table_idx")
+    if table_idx.shape[0] != batch:
+        raise ValueError("table_idx must have batch entries")
+    return pp, sp, tp, stride
+
+
+def _ints(t, n: int, dev: int, name: str) -> int:
+    """Address of an int32 tensor of n entries."""
+    p = _arg(t, torch.int32, 1, dev, name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return p
+
+
+def _workspace(workspace, dev: int):
+    """(address, bytes) of a workspace tensor or None."""
     if workspace is None:
         return None, 0
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
     _contig(workspace, "workspace")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -247,47 +283,37 @@ def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc,
     append k and v to the pool at out_loc [N]; rows may be strided (slices of a fused projection).
     cos_sin [positions, rot_dim] fp32, cosines first, or None (no rotation: positions may be None);
     q_norm, k_norm [D] bf16 weights or None. q and q_out None: append only."""
-    ps = pool_struct(pool)
-    n, hkv, d = k.shape
-    if hkv != ps.num_kv_heads or d != ps.head_dim or v.shape != k.shape:
-        raise ValueError("k and v must be [N, Hkv, D] with the pool's heads and dims")
-    for t, name in ((k, "k"), (v, "v")):
-        _want(t, torch.bfloat16, name, 3)
-    ks = _row_stride(k, "k")
-    if _row_stride(v, "v") != ks:
+    dev = torch.cuda.current_device()
+    ps = _pool_arg(pool, dev)
+    n, d = k.shape[0], ps.head_dim
+    kv_shape = (n, ps.num_kv_heads, d)
+    kp, ks = _rows_arg(k, kv_shape, dev, "k")
+    vp, vs = _rows_arg(v, kv_shape, dev, "v")
+    if vs != ks:
         raise ValueError("k and v rows must share a row stride")
-    _want(out_loc, torch.int32, "out_loc", 1)
-    _contig(out_loc, "out_loc")
-    if out_loc.shape[0] != n:
-        raise ValueError("out_loc must have one slot per token")
-    hq = qs = 0
+    qp = op = tp = pp = qn = kn = None
+    hq = qs = rot = rows = 0
     if q is not None:
-        _want(q, torch.bfloat16, "q", 3)
-        _want(q_out, torch.bfloat16, "q_out", 3)
-        _contig(q_out, "q_out")
-        if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
-            raise ValueError("q and q_out must be [N, Hq, D] with k's tokens and dims")
-        hq, qs = q.shape[1], _row_stride(q, "q")
-    rot = table = 0
+        hq = q.shape[1]
+        qp, qs = _rows_arg(q, (n, hq, d), dev, "q")
+        op = _arg(q_out, torch.bfloat16, 3, dev, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must match q")
     if cos_sin is not None:
-        _want(cos_sin, torch.float32, "cos_sin", 2)
-        _contig(cos_sin, "cos_sin")
-        _want(positions, torch.int32, "positions", 1)
-        _contig(positions, "positions")
-        table, rot = cos_sin.shape
-        if positions.shape[0] != n:
-            raise ValueError("positions must have one entry per token")
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _want(w, torch.bfloat16, name, 1)
-            _contig(w, name)
-            if w.shape[0] != d:
-                raise ValueError(f"{name} must have head_dim entries")
-    _one_device(pool, k, v, out_loc, q, q_out, cos_sin, positions if rot else None, q_norm, k_norm)
+        tp = _arg(cos_sin, torch.float32, 2, dev, "cos_sin")
+        rows, rot = cos_sin.shape
+        pp = _ints(positions, n, dev, "positions")
+    if q_norm is not None:
+        qn = _arg(q_norm, torch.bfloat16, 1, dev, "q_norm")
+        if q_norm.shape[0] != d:
+            raise ValueError("q_norm must have head_dim entries")
+    if k_norm is not None:
+        kn = _arg(k_norm, torch.bfloat16, 1, dev, "k_norm")
+        if k_norm.shape[0] != d:
+            raise ValueError("k_norm must have head_dim entries")
     _check(load().pkv_norm_rope_kv_store(
-        ctypes.byref(ps), int(layer), _ptr(q), qs, _ptr(q_out), hq, _ptr(k), _ptr(v), ks,
-        _ptr(q_norm), _ptr(k_norm), float(eps), _ptr(cos_sin), table, rot, int(bool(interleaved)),
-        _ptr(positions) if rot else None, _ptr(out_loc), n, _stream(stream)))
+        ctypes.byref(ps), layer, qp, qs, op, hq, kp, vp, ks, qn, kn, eps, tp, rows, rot,
+        bool(interleaved), pp, _ints(out_loc, n, dev, "out_loc"), n, _stream(stream)))
 
 
 def pkv_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -323,18 +349,16 @@ def pkv_paged_decode_attn(pool, layer: int, q, o, lse, page_table, seq_lens, sca
         int(max_seq_len_hint), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int) -> PkvScoreMod:
+def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,
+               dev: int) -> PkvScoreMod:
+    sp = pp = None
     if alibi_slopes is not None:
-        _want(alibi_slopes, torch.float32, "alibi_slopes", 1)
-        _contig(alibi_slopes, "alibi_slopes")
+        sp = _arg(alibi_slopes, torch.float32, 1, dev, "alibi_slopes")
         if alibi_slopes.shape[0] != hq:
             raise ValueError("alibi_slopes must have one entry per q head")
     if prefix_lens is not None:
-        _want(prefix_lens, torch.int32, "prefix_lens", 1)
-        _contig(prefix_lens, "prefix_lens")
-        if prefix_lens.shape[0] != batch:
-            raise ValueError("prefix_lens must have batch entries")
-    return PkvScoreMod(float(soft_cap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens))
+        pp = _ints(prefix_lens, batch, dev, "prefix_lens")
+    return PkvScoreMod(soft_cap, sp, window, pp)
 
 
 def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens, scale: float,
@@ -344,20 +368,18 @@ def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens,
     """Decode attention under score rules: a soft cap, alibi_slopes [Hq] fp32, a window, and
     prefix_lens [B] int32 first keys that stay visible. max_keys_hint: a bound on the keys a
     request sees (min(seq_len, window + prefix) with a window)."""
-    ps = pool_struct(pool)
-    B, Hq, _ = q.shape
-    _queries(ps, q, o, lse)
-    _tables(page_table, seq_lens, table_idx, B)
-    if seq_lens.shape[0] != B:
-        raise ValueError("seq_lens must have batch entries")
-    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq)
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(pool, q, o, lse, page_table, seq_lens, table_idx, alibi_slopes, prefix_lens,
-                workspace)
+    dev = torch.cuda.current_device()
+    ps = _pool_arg(pool, dev)
+    qp, op, lp = _queries(q, o, lse, dev)
+    B, Hq, D = q.shape
+    if D != ps.head_dim:
+        raise ValueError("q must have the pool's head_dim")
+    pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
+    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_decode_attn_mod(
-        ctypes.byref(ps), int(layer), _ptr(q), _ptr(o), _ptr(lse), _ptr(page_table),
-        page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, Hq, float(scale),
-        ctypes.byref(mod), int(max_keys_hint), ws, ws_bytes, _stream(stream)))
+        ctypes.byref(ps), layer, qp, op, lp, pp, stride, tp, sp, B, Hq, scale, ctypes.byref(mod),
+        max_keys_hint, ws, ws_bytes, _stream(stream)))
 
 
 def pkv_paged_decode_attn_store(pool, layer: int, q, k_new, v_new, o, lse, page_table, seq_lens,
@@ -473,23 +495,19 @@ def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table
     """Extend attention under score rules (as pkv_paged_decode_attn_mod's), chunk query j of
     request r at position seq_lens[r] - c_r + j; prefix_lens also lets the queries inside the
     prefix see the keys behind them."""
-    ps = pool_struct(pool)
-    T, Hq, _ = q.shape
+    dev = torch.cuda.current_device()
+    ps = _pool_arg(pool, dev)
+    qp, op, lp = _queries(q, o, lse, dev)
+    T, Hq, D = q.shape
+    if D != ps.head_dim:
+        raise ValueError("q must have the pool's head_dim")
     B = seq_lens.shape[0]
-    _queries(ps, q, o, lse)
-    _tables(page_table, seq_lens, table_idx, B)
-    _want(qo_indptr, torch.int32, "qo_indptr", 1)
-    _contig(qo_indptr, "qo_indptr")
-    if qo_indptr.shape[0] != B + 1:
-        raise ValueError("qo_indptr must have batch+1 entries")
-    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq)
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(pool, q, o, lse, qo_indptr, page_table, seq_lens, table_idx, alibi_slopes,
-                prefix_lens, workspace)
+    pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
+    mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_extend_attn_mod(
-        ctypes.byref(ps), int(layer), _ptr(q), _ptr(qo_indptr), _ptr(o), _ptr(lse),
-        _ptr(page_table), page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, T, Hq,
-        float(scale), ctypes.byref(mod), int(max_seq_len_hint), int(max_total_keys_hint), ws,
+        ctypes.byref(ps), layer, qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"), op, lp, pp, stride,
+        tp, sp, B, T, Hq, scale, ctypes.byref(mod), max_seq_len_hint, max_total_keys_hint, ws,
         ws_bytes, _stream(stream)))
 
 
@@ -547,22 +565,19 @@ def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_ta
     """Attention of drafted tokens: q, o [T, Hq, D] bf16, qo_indptr [B+1] and parents [T] int32
     (index within the request, -1 for a root); lse [T, Hq] fp32 or None; seq_lens count the
     drafted tokens, whose keys are in the pool."""
-    ps = pool_struct(pool)
+    dev = torch.cuda.current_device()
+    ps = _pool_arg(pool, dev)
+    qp, op, lp = _queries(q, o, lse, dev)
     T, Hq, D = q.shape
+    if D != ps.head_dim:
+        raise ValueError("q must have the pool's head_dim")
     B = seq_lens.shape[0]
-    _queries(ps, q, o, lse)
-    _tables(page_table, seq_lens, table_idx, B)
-    for t, name, n in ((qo_indptr, "qo_indptr", B + 1), (parents, "parents", T)):
-        _want(t, torch.int32, name, 1)
-        _contig(t, name)
-        if t.shape[0] != n:
-            raise ValueError(f"{name} must have {n} entries")
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(pool, q, o, lse, qo_indptr, parents, page_table, seq_lens, table_idx, workspace)
+    pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_tree_attn(
-        ctypes.byref(ps), int(layer), _ptr(q), _ptr(qo_indptr), _ptr(parents), _ptr(o), _ptr(lse),
-        _ptr(page_table), page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, T, Hq,
-        float(scale), int(max_tree_tokens), int(max_seq_len_hint), ws, ws_bytes, _stream(stream)))
+        ctypes.byref(ps), layer, qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"),
+        _ints(parents, T, dev, "parents"), op, lp, pp, stride, tp, sp, B, T, Hq, scale,
+        max_tree_tokens, max_seq_len_hint, ws, ws_bytes, _stream(stream)))
 
 
 def pkv_cascade_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

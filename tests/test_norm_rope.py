@@ -225,10 +225,23 @@ def test_no_tokens_is_a_no_op():
     assert _call(binding.load(), pool, n=0, k=None, v=None, q=None) == 0
 
 
-def test_binding_checks_shapes_before_the_library():
+@pytest.mark.gpu
+def test_binding_checks_tensors_before_the_library():
     import paged_kv_attention_out_gb300 as pkv
-    pool = torch.zeros(2, 1, 2, 4, 2, 64, dtype=torch.bfloat16)
-    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
-    with pytest.raises(TypeError):  # CPU tensors
-        pkv.pkv_norm_rope_kv_store(pool, 0, None, k, k, None, None,
-                                   torch.zeros(3, dtype=torch.int32))
+    pool, q, k, v, w, table, pos, loc = setup(6, 4, 2, 64, 1, 64, True)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+
+    def call(**kw):
+        a = dict(pool=pool, q=q, k=k, v=v, q_out=q_out, positions=pos, out_loc=loc, cos_sin=table)
+        a.update(kw)
+        pkv.pkv_norm_rope_kv_store(layer=0, **a)
+
+    for kw in (dict(k=k.cpu()), dict(v=v.float()), dict(out_loc=loc.long()),
+               dict(cos_sin=table.double()), dict(pool=pool.half())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(k=k[:5]), dict(v=v[:, :1]), dict(out_loc=loc[:5]), dict(positions=pos[::2]),
+               dict(q_out=q_out[:, :2].contiguous()), dict(q_out=q_out.transpose(0, 1)),
+               dict(k=k.transpose(1, 2).contiguous().transpose(1, 2)), dict(q_norm=w[0][:32])):
+        with pytest.raises(ValueError):
+            call(**kw)
