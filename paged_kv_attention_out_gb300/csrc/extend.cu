@@ -546,19 +546,6 @@ __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
   return true;
 }
 
-// TMA tile load (as tma_load_2d) with an L2 eviction-priority policy
-// (createpolicy): the K/V workspace tiles are read again by every block of
-// their request, so they are kept (evict last) ahead of Q and O, which are
-// touched once.
-__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void *tmap, int x, int y,
-                                                 uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 // ------------------------------------------------------------ attention
 // One CTA per SM pulls work items, (kv head, block) pairs in longest-first
 // order, from a counter the planner zeroes (plan[1]); item i is block

@@ -278,6 +278,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int 
       : "memory");
 }
 
+// The same with an L2 eviction-priority policy (createpolicy): tiles that are
+// read again soon are kept (evict last), those read once go first.
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void *tmap, int x, int y,
+                                                 uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // TMA tile load of a 3-D box (coordinates x innermost, then y, z) into
 // shared memory at dst, laid out as the box's rows of 128 bytes in (z, y)
 // order with the map's swizzle. Completion counts the box's bytes down on

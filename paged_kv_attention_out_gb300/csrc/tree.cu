@@ -13,25 +13,30 @@
 // rows (tokens x the g query heads of one kv head): 2 * rows FLOPs per byte,
 // so memory up to a hundred rows or so, and near the softmax's rate at 256.
 //
-// Schedule. The unit of work is a 128-key tile of one query block. Group i of
-// G = SMs / Hkv groups takes the i-th equal share of all units, in (block, key)
-// order; the Hkv CTAs of a group walk the same share, one kv head each, so the
-// pieces of a token's K (V) row are read at about the same time. Every group
-// has the same number of tiles whatever the requests' lengths are, and only
-// its first and last block can be shared with a neighbour: those go out as
-// fp32 partial states (slots 2 i and 2 i + 1 of the workspace) and a second
-// kernel merges them; every other block is written directly.
+// Schedule. The unit of work is a 128-key tile of one query block, with a cost
+// of its own where two query tiles share it. Group i of G = SMs / Hkv groups
+// takes the i-th equal share of the cost of all units, in (block, key) order;
+// the Hkv CTAs of a group walk the same share, one kv head each, so the pieces
+// of a token's K (V) row are read at about the same time. Every group has the
+// same work whatever the requests' lengths are, and only its first and last
+// block can be shared with a neighbour: those go out as fp32 partial states
+// (slot 2 i of the workspace for a block begun by an earlier group, 2 i + 1
+// for one that goes on in the next) and a second kernel merges them; every
+// other block is written directly.
 //
 // Roles of a CTA (kQT = 1 or 2 query tiles of 128 rows):
 //   warps 0 .. 4 kQT - 1  softmax: one query row per thread (TMEM lane)
 //   next warp             TMEM allocation and the single MMA-issuing thread
 //   the rest              producers: the Q tiles by TMA, then K and V tiles
-//       alternately into a ring of slots; kTma: one warp, TMA boxes of kBox
-//       rows (a power of two dividing the page size), the box holding the
+//       alternately into a ring of slots; kTma: three warps, TMA boxes of a
+//       power of two of rows that divides the page size, the box holding the
 //       request's last key by 16-byte cp.async with zero fill, so that no
 //       stale bits behind it reach P V; otherwise two or four warps of cp.async.
 // With one query tile the scores are double buffered, S(j + 1) is computed
-// while the softmax works on S(j); with two, the tiles take turns.
+// while the softmax works on S(j); with two, the tiles take turns. A block of
+// the two-tile kernel whose tokens fit one tile is walked by both softmax
+// groups, each taking every other key tile with a state of its own (m, l, O),
+// which the first group joins at the end of the segment.
 // Every hand-off is an mbarrier; every wait is bounded (tc_common.cuh).
 #include <cuda.h>
 #include <math.h>
@@ -55,19 +60,30 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxTree = PKV_MAX_TREE_TOKENS;
 constexpr int kMaskWords = kMaxTree / 32;
 constexpr int kMinTiles = 2;  // smallest share of a group: two key tiles
+// Cost of a key tile for a block of one and of two query tiles.
+#ifndef PKV_TREE_COST1
+#define PKV_TREE_COST1 3
+#endif
+#ifndef PKV_TREE_COST2
+#define PKV_TREE_COST2 5
+#endif
+constexpr int kCost1 = PKV_TREE_COST1, kCost2 = PKV_TREE_COST2;
 constexpr int kMergeRows = 32;
 
-// Producer warps. Two query tiles leave registers for ten or eleven warps
-// whose softmax threads hold a whole score row each.
+// Producer warps: with two query tiles the CTA's twelfth warp is the last that
+// costs no registers (a softmax thread holds a whole score row). By TMA each
+// warp issues every third K or V tile: a warp's issue of boxes of 16 rows, one
+// lane after the other, takes longer than their bytes do (page size 16, one
+// query tile: 185 us with one warp).
 constexpr int producer_warps(int query_tiles, bool tma) {
-  return tma ? 1 : (query_tiles == 2 ? 2 : 4);
+  return tma ? 3 : (query_tiles == 2 ? 2 : 4);
 }
 
 template <int D, int kQT>
 struct TreeSmem {
   static constexpr int kQBytes = kM * D * 2;   // one query tile
   static constexpr int kSlotBytes = kN * D * 2;  // one K or V tile
-  static constexpr int kSlots = D == 128 ? (kQT == 2 ? 4 : 6) : 8;
+  static constexpr int kSlots = D == 128 ? (kQT == 2 ? 5 : 6) : 8;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQT * kQBytes;
   static constexpr int kBars = kRing + kSlots * kSlotBytes;
@@ -88,7 +104,8 @@ enum : int {
   kBarOEmpty = 23,    // [2] softmax: O_x read out
   kBarQFull = 25,     // producer: Q landed
   kBarQEmpty = 26,    // MMA: every S of the segment done
-  kBarTeardown = 27,
+  kBarState = 27,     // softmax group 1: its state of a shared query tile is in shared memory
+  kBarTeardown = 28,
 };
 
 struct TreeArgs {
@@ -118,13 +135,14 @@ struct TreeArgs {
   int32_t q_mode;        // 0: scores as they are, 1: negated (scale < 0), 2: zero (scale 0)
   float *part_o;         // [2 groups][Hkv][D / 4][rows] float4
   float *part_lse;       // [2 groups][Hkv][rows]
-  int2 *table;           // per block: {slot of its first segment, last group}, {-1, 0}: no merge
+  int2 *table;           // per block: its first and last group, {-1, -1} if nothing is merged
   unsigned *err;
 };
 
 // One query block: up to kQT tokens_per_tile tokens of one request.
 struct Block {
   int req, sub, t_base, tokens, p, c, seq, tiles;
+  int cost;  // of a key tile
 };
 
 // Block b of the call, tiles = 0 if there is nothing to compute. Keys behind
@@ -152,6 +170,7 @@ __device__ __forceinline__ Block load_block(const TreeArgs &a, int b, bool repor
   }
   k.t_base = beg + k.sub * tpb;
   k.tokens = min(tpb, k.c - k.sub * tpb);
+  k.cost = k.tokens <= a.tokens_per_tile ? kCost1 : kCost2;
   k.tiles = k.tokens > 0 ? (k.p + k.sub * tpb + k.tokens + kN - 1) / kN : 0;
   return k;
 }
@@ -160,8 +179,7 @@ __device__ __forceinline__ Block load_block(const TreeArgs &a, int b, bool repor
 struct Walk {
   int block;      // of the next segment
   int skip;       // tiles of it that belong to an earlier group
-  int64_t left;   // tiles of the share not walked yet
-  int index;      // segments so far
+  int64_t left;   // cost of the share from the next tile on
 };
 
 struct Segment {
@@ -173,27 +191,34 @@ struct Segment {
 
 template <int kQT>
 __device__ __forceinline__ bool next_segment(const TreeArgs &a, Walk &w, Segment &s) {
-  if (w.left <= 0) return false;
   const int nblocks = a.batch * a.blocks_per_req;
-  while (w.block < nblocks) {
+  while (w.block < nblocks && w.left > 0) {
     s.b = load_block<kQT>(a, w.block, false);
     ++w.block;
-    if (s.b.tiles == 0) continue;
     s.tile0 = w.skip;
     w.skip = 0;
-    s.n = static_cast<int>(min(static_cast<int64_t>(s.b.tiles - s.tile0), w.left));
+    if (s.tile0 >= s.b.tiles) continue;
+    // the tiles that begin within the share
+    s.n = static_cast<int>(min(static_cast<int64_t>(s.b.tiles - s.tile0),
+                               (w.left + s.b.cost - 1) / s.b.cost));
     s.whole = s.n == s.b.tiles;
-    s.slot = 2 * static_cast<int>(blockIdx.y) + (w.index > 0 ? 1 : 0);
-    w.left -= s.n;
-    ++w.index;
+    s.slot = 2 * static_cast<int>(blockIdx.y) + (s.tile0 == 0 ? 1 : 0);
+    w.left -= static_cast<int64_t>(s.n) * s.b.cost;
     return true;
   }
   return false;
 }
 
-// Key tiles that query tile x walks of the segment: all that may hold a key
-// its tokens see.
+// Whether the two softmax groups of the two-tile kernel share the block's one
+// query tile (group x takes key tiles x, x + 2, ..) or have a tile each.
+__device__ __forceinline__ bool shared_tile(const TreeArgs &a, const Segment &s) {
+  return s.b.tokens <= a.tokens_per_tile && s.n > 1;
+}
+
+// Key tiles that softmax group x walks of the segment (two-tile kernel): its
+// share of them, or all that may hold a key its query tile's tokens see.
 __device__ __forceinline__ int tiles_of(const TreeArgs &a, const Segment &s, int tpb, int x) {
+  if (shared_tile(a, s)) return (s.n + 1 - x) / 2;
   const int tok = min(a.tokens_per_tile, s.b.tokens - x * a.tokens_per_tile);
   if (tok <= 0) return 0;
   const int end = (s.b.p + s.b.sub * tpb + x * a.tokens_per_tile + tok + kN - 1) / kN;
@@ -223,7 +248,8 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   __shared__ int s_abort;
   __shared__ long long s_scan[kThreads / 32];
   __shared__ Walk s_walk;
-  __shared__ uint8_t s_parents[kSoftmaxWarps][kMaxTree];  // a copy for each warp; root: 255
+  __shared__ float2 s_state[kQT == 2 ? kM : 1];  // (m, l) of group 1's rows (shared query tile)
+  __shared__ uint8_t s_parents[kQT][kMaxTree];  // a copy for each softmax group; root: 255
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -240,7 +266,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kBarFull + i), kProducerWarps * 32);
+      mbar_init(bar(kBarFull + i), (kTma ? 1 : kProducerWarps) * 32);
       mbar_init(bar(kBarEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -252,9 +278,10 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     mbar_init(bar(kBarPvDone), 1);
     mbar_init(bar(kBarQFull), 1);
     mbar_init(bar(kBarQEmpty), 1);
+    mbar_init(bar(kBarState), 128);
     mbar_init(bar(kBarTeardown), 1);
     s_abort = 0;
-    s_walk = Walk{0, 0, 0, 0};
+    s_walk = Walk{0, 0, 0};
     mbar_init_fence();
   }
   {
@@ -272,9 +299,9 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   grid_dependency_wait();  // pool, q and tables may come from the previous kernel
   grid_dependents_launch();
   {
-    // The share of this CTA's group: the total of all blocks' tiles, then the
-    // block that holds the share's first tile. Thread t of a round takes
-    // block base + t.
+    // The share of this CTA's group: the total cost of all blocks, then the
+    // block that holds the share's beginning. Thread t of a round takes block
+    // base + t.
     const int nblocks = a.batch * a.blocks_per_req;
     const bool lead = blockIdx.x == 0 && blockIdx.y == 0;
     auto scan = [&](long long v, long long &total) {  // inclusive, over the CTA
@@ -296,34 +323,48 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       return v + before;
     };
     long long total = 0, round;
-    const int mine = tid < nblocks ? load_block<kQT>(a, tid, lead).tiles : 0;
+    auto cost_of = [&](int b, bool report, int &cost) -> long long {
+      cost = 1;
+      if (b >= nblocks) return 0;
+      const Block k = load_block<kQT>(a, b, report);
+      cost = max(k.cost, 1);
+      return static_cast<long long>(k.tiles) * k.cost;
+    };
+    int unit0, unit;
+    const long long mine = cost_of(tid, lead, unit0);
     const long long first_end = scan(mine, round);
     const long long first_total = round;
     total = round;
     for (int b0 = kThreads; b0 < nblocks; b0 += kThreads) {
-      scan(b0 + tid < nblocks ? load_block<kQT>(a, b0 + tid, lead).tiles : 0, round);
+      scan(cost_of(b0 + tid, lead, unit), round);
       total += round;
     }
-    const long long per = max(static_cast<long long>(kMinTiles), (total + a.groups - 1) / a.groups);
+    // at least one tile begins in every share that a block covers
+    const long long per = max(static_cast<long long>(max(kMinTiles * kCost1, kCost2)),
+                              (total + a.groups - 1) / a.groups);
     const long long lo = per * blockIdx.y;
     const long long hi = min(total, lo + per);
     long long base = 0;
     for (int b0 = 0; b0 < nblocks && (lead || base <= lo); b0 += kThreads) {
       const int b = b0 + tid;
-      const int tiles = b0 == 0 ? mine : (b < nblocks ? load_block<kQT>(a, b, false).tiles : 0);
+      long long cost = mine;
+      unit = unit0;
+      if (b0 > 0) cost = cost_of(b, false, unit);
       long long end = first_end;
       round = first_total;
-      if (b0 > 0) end = scan(tiles, round);
+      if (b0 > 0) end = scan(cost, round);
       end += base;
-      const long long start = end - tiles;
-      if (tiles > 0 && start <= lo && lo < end && lo < hi)
-        s_walk = Walk{b, static_cast<int>(lo - start), hi - lo, 0};
+      const long long start = end - cost;
+      if (cost > 0 && start <= lo && lo < end && lo < hi) {
+        const long long skip = (lo - start + unit - 1) / unit;
+        s_walk = Walk{b, static_cast<int>(skip), hi - (start + skip * unit)};
+      }
       if (lead && b < nblocks && a.groups > 1) {
-        // which groups the block's tiles fall to (the merge reads this)
-        int2 e = make_int2(-1, 0);
-        if (tiles > 0) {
-          const int g0 = static_cast<int>(start / per), g1 = static_cast<int>((end - 1) / per);
-          if (g1 > g0) e = make_int2(2 * g0 + (start % per != 0 ? 1 : 0), g1);
+        // which groups the block's tiles begin in (the merge reads this)
+        int2 e = make_int2(-1, -1);
+        if (cost > 0) {
+          const int g0 = static_cast<int>(start / per), g1 = static_cast<int>((end - unit) / per);
+          if (g1 > g0) e = make_int2(g0, g1);
         }
         a.table[b] = e;
       }
@@ -342,8 +383,11 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     const int pw = warp - kProducerWarp0;
     const int64_t row_elems = static_cast<int64_t>(a.hkv) * D;
     const int64_t head_off = static_cast<int64_t>(kvh) * D;
-    const uint64_t kv_policy = l2_evict_first_policy();  // a byte is read once per block
-    constexpr int kGroups = kTma ? 1 : kN / (32 * kProducerWarps);
+    // A byte is read once per block: with one block per request its lines go
+    // first (page size 64: 144.7 us against 150.2 with the default policy).
+    const uint64_t kv_policy = a.blocks_per_req == 1 ? l2_evict_first_policy()
+                                                     : l2_evict_normal_policy();
+    constexpr int kGroups = kTma ? 1 : kN / (32 * kProducerWarps);  // keys per lane and tile
     constexpr int kChunks = D / 8;
     constexpr int kKeysPerInstr = 32 / kChunks;
     const int ch = lane % kChunks;
@@ -353,31 +397,35 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     while (ok && next_segment<kQT>(a, walk, sg)) {
       const int row = a.table_idx ? a.table_idx[sg.b.req] : sg.b.req;
       const int32_t *pages = a.page_table + static_cast<int64_t>(row) * a.table_stride;
-      // first pool row of key `key`'s box, -1 past the request or for a bad page
-      auto slot_of = [&](int key, int rows) -> long long {
-        if (key >= sg.b.seq) return -1;
-        const int pi = key / a.page_size;
-        const int ent = __ldg(pages + pi);
-        const long long s = static_cast<long long>(ent) * a.page_size + (key - pi * a.page_size);
-        if (ent < 0 || s + rows > a.slots) {
+      // This lane's boxes of tile j (kTma: box `lane` of the tile; otherwise
+      // one key of each 32 the warp copies): the page entry, loaded a tile
+      // ahead and looked at only when the tile's copies are issued, and the
+      // first pool row (-1 past the request or for a bad page).
+      const int box = kTma ? a.box : 1;
+      auto box_key = [&](int j, int g) -> int {
+        const int at = kTma ? lane * box : (pw * kGroups + g) * 32 + lane;
+        const int key = (sg.tile0 + j) * kN + at;
+        return at < kN && key < sg.b.seq ? key : -1;
+      };
+      auto load_entries = [&](int j, int (&e)[kGroups]) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const int key = box_key(j, g);
+          e[g] = key >= 0 ? __ldg(pages + key / a.page_size) : -1;
+        }
+      };
+      auto first_row = [&](int j, int g, int ent) -> long long {
+        const int key = box_key(j, g);
+        if (key < 0) return -1;
+        const long long s = static_cast<long long>(ent) * a.page_size + key % a.page_size;
+        if (ent < 0 || s + box > a.slots) {
           flag_error(a.err, kErrPage);
           return -1;
         }
         return s;
       };
-      // This lane's boxes (kTma: box `lane` of the tile; otherwise one key of
-      // each 32 the warp copies) of tile j: their first pool rows.
-      const int box = kTma ? a.box : 1;
-      auto load_slots = [&](int j, long long (&s)[kGroups]) {
-        const int key0 = (sg.tile0 + j) * kN;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const int at = kTma ? lane * box : (pw * kGroups + g) * 32 + lane;
-          s[g] = at < kN ? slot_of(key0 + at, box) : -1;
-        }
-      };
-      long long next[kGroups], cur[kGroups];
-      load_slots(0, next);
+      int next[kGroups];
+      load_entries(0, next);
       if (pw == 0) {
         if (segs > 0) ok = mbar_wait_warp(bar(kBarQEmpty), (segs - 1) & 1, abort);
         if (ok && lane == 0) {
@@ -397,11 +445,13 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       ++segs;
       for (int j = 0; ok && j < sg.n; ++j) {
         const int key0 = (sg.tile0 + j) * kN;
+        long long cur[kGroups];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) cur[g] = next[g];
-        if (j + 1 < sg.n) load_slots(j + 1, next);  // off the copy path
+        for (int g = 0; g < kGroups; ++g) cur[g] = first_row(j, g, next[g]);
+        if (j + 1 < sg.n) load_entries(j + 1, next);
 #pragma unroll
         for (int c = 0; c < 2; ++c, ++u) {
+          if (kTma && u % kProducerWarps != static_cast<uint32_t>(pw)) continue;
           const int st = static_cast<int>(u % kSlots);
           if (u >= kSlots &&
               !(ok = mbar_wait_warp(bar(kBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
@@ -423,9 +473,9 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
             if (live) {
 #pragma unroll
               for (int h = 0; h < kHalves; ++h)
-                tma_load_2d(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
-                            c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
-                            bar(kBarFull + st));
+                tma_load_2d_hint(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
+                                 c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
+                                 bar(kBarFull + st), kv_policy);
             }
             while (rest) {
               const int src = __ffs(rest) - 1;
@@ -456,13 +506,14 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     }
     if (!ok) *abort = 1;
     cp_async_wait_all();
-    if (*abort && lane == 0 && pw == 0) {
-      // every issued TMA copy lands before the CTA can exit
+    if (*abort && lane == 0) {
+      // every TMA copy this warp issued lands before the CTA can exit
       int never = 0;
-      if (segs > 0) mbar_wait(bar(kBarQFull), (segs - 1) & 1, &never);
+      if (pw == 0 && segs > 0) mbar_wait(bar(kBarQFull), (segs - 1) & 1, &never);
       if (kTma)
         for (uint32_t t = u > kSlots ? u - kSlots : 0; t < u; ++t)
-          mbar_wait(bar(kBarFull + t % kSlots), (t / kSlots) & 1, &never);
+          if (t % kProducerWarps == static_cast<uint32_t>(pw))
+            mbar_wait(bar(kBarFull + t % kSlots), (t / kSlots) & 1, &never);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -510,24 +561,33 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         const int n = sg.n;
         if (!(ok = mbar_wait_fast(bar(kBarQFull), segs & 1, abort))) break;
         ++segs;
-        if (kQT == 1) {
+        // One query tile: key tiles alternate between the score buffers, and
+        // (two-tile kernel) between the softmax groups and their O.
+        const bool alternate = kQT == 1 || shared_tile(a, sg);
+        if (alternate) {
           for (int j = 0; ok && j < 2 && j < n; ++j) {
             if (!(ok = wait_unit(u0 + 2 * j))) break;
             qk(0, j, u0 + 2 * j);
             free_unit(u0 + 2 * j);
           }
           if (n <= 2 && ok) umma_commit(bar(kBarQEmpty));
-          if (ok && uses0 > 0) ok = mbar_wait_fast(bar(kBarOEmpty), (uses0 - 1) & 1, abort);
           for (int j = 0; ok && j < n; ++j) {
             const int buf = j & 1;
+            const int x = kQT == 2 ? buf : 0;
             uint32_t &np = buf ? np1 : np0;
+            const uint32_t uses = x ? uses1 : uses0;
+            const bool first = j <= x;  // of O_x
+            if (first && uses > 0 &&
+                !(ok = mbar_wait_fast(bar(kBarOEmpty + x), (uses - 1) & 1, abort)))
+              break;
             if (!(ok = mbar_wait_fast(bar(kBarPFull + buf), np & 1, abort) &&
                        wait_unit(u0 + 2 * j + 1)))
               break;
             ++np;
-            pv(0, buf, u0 + 2 * j + 1, j == 0);
+            pv(x, buf, u0 + 2 * j + 1, first);
             free_unit(u0 + 2 * j + 1);
-            umma_commit(bar(kBarPvDone));
+            if (kQT == 1) umma_commit(bar(kBarPvDone));
+            if (kQT == 2 && j + 2 >= n) umma_commit(bar(kBarOFull + x));
             if (j + 2 < n) {
               if (!(ok = wait_unit(u0 + 2 * (j + 2)))) break;
               qk(0, buf, u0 + 2 * (j + 2));
@@ -535,8 +595,9 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
               if (j + 3 == n) umma_commit(bar(kBarQEmpty));
             }
           }
-          if (ok) umma_commit(bar(kBarOFull));
+          if (kQT == 1 && ok) umma_commit(bar(kBarOFull));
           ++uses0;
+          if (kQT == 2) ++uses1;
         } else {
           const int n0 = tiles_of(a, sg, tpb, 0), n1 = tiles_of(a, sg, tpb, 1);
           // score tile j of both query tiles, for those that walk it
@@ -599,19 +660,26 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     const uint32_t orow_t = tmem + lane_base + kTmemO + x * kN;
     uint32_t ns0 = 0, ns1 = 0;  // score tiles taken (per buffer with one query tile)
     uint32_t pv_tiles = 0;      // tiles before this segment (one query tile)
-    uint32_t uses = 0;          // segments that used O_x
+    uint32_t uses[2] = {0, 0};  // segments that used O_0, O_1
+    uint32_t states = 0;        // shared query tiles so far
     bool ok = true;
     while (ok && next_segment<kQT>(a, walk, sg)) {
+      const bool shared = kQT == 2 && shared_tile(a, sg);
+      const int xq = shared ? 0 : x;  // query tile
       const int n_x = kQT == 1 ? sg.n : tiles_of(a, sg, tpb, x);
-      const int tok = x * tpt + tt;  // token within the block
+      const int n_other = kQT == 1 ? 0 : tiles_of(a, sg, tpb, 1 - x);
+      const int tok = xq * tpt + tt;  // token within the block
       const bool valid = tt < tpt && tok < sg.b.tokens;
       const int first_draft = sg.b.p;
       // This row's ancestors (bit i: drafted key i), if the segment reaches
-      // the drafted keys; every warp loads the request's parents for itself.
+      // the drafted keys. Every warp writes the request's parents (the same
+      // ones) and reads back what it wrote; the group's other warps are done
+      // with the last ones, since they were all waited for at that segment's
+      // end (its final O takes every warp's P).
       uint32_t anc[kMaskWords];
 #pragma unroll
       for (int w = 0; w < kMaskWords; ++w) anc[w] = 0;
-      if ((sg.tile0 + sg.n) * kN > first_draft) {
+      if (n_x > 0 && (sg.tile0 + sg.n) * kN > first_draft) {
         __syncwarp();  // the previous segment's are read
         for (int i = lane; i < sg.b.c; i += 32) {
           int par = a.parents[sg.b.t_base - sg.b.sub * tpb + i];
@@ -619,7 +687,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
             flag_error(a.err, kErrTree);
             par = -1;
           }
-          s_parents[warp][i] = static_cast<uint8_t>(par < 0 ? 255 : par);
+          s_parents[x][i] = static_cast<uint8_t>(par < 0 ? 255 : par);
         }
         __syncwarp();
         if (valid) {
@@ -628,7 +696,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
           for (int i = sg.b.sub * tpb + tok;;) {
 #pragma unroll
             for (int w = 0; w < kMaskWords; ++w) anc[w] |= (i >> 5) == w ? 1u << (i & 31) : 0u;
-            i = s_parents[warp][i];
+            i = s_parents[x][i];
             if (i == 255) break;
           }
         }
@@ -647,7 +715,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         tmem_ld32_max(srow + 64, *reinterpret_cast<float(*)[32]>(&v[64]), mx2);
         tmem_ld32_max(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
         tmem_ld_wait();
-        const int key0 = (sg.tile0 + j) * kN;
+        const int key0 = (sg.tile0 + (shared ? 2 * j + x : j)) * kN;
         const bool masked = key0 + kN > first_draft;  // uniform over the CTA
         if (masked || a.q_mode) {
           if (a.q_mode) {
@@ -744,27 +812,63 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       if (!ok) break;
       pv_tiles += static_cast<uint32_t>(sg.n);
       if (n_x > 0) {
-        if (!(ok = mbar_wait_warp(bar(kBarOFull + x), uses & 1, abort))) break;
-        ++uses;
-        tc_fence_after_sync();
+        if (!(ok = mbar_wait_warp(bar(kBarOFull + x), uses[x] & 1, abort))) break;
+        ++uses[x];
       }
+      float f0 = 1.f, f1 = 0.f;  // factors of O_0 (this group's) and O_1
+      if (kQT == 2) {
+        if (shared && x == 1) {
+          // O_1 and its state are the first group's to join, and to hand back
+          s_state[r] = make_float2(m_used, l);
+          tc_fence_before_sync();
+          mbar_arrive(bar(kBarState));
+          if (n_other > 0) ++uses[0];
+          ++states;
+          continue;
+        }
+        if (shared) {
+          if (!(ok = mbar_wait_warp(bar(kBarState), states & 1, abort) &&
+                     mbar_wait_warp(bar(kBarOFull + 1), uses[1] & 1, abort)))
+            break;
+          ++states;
+          const float2 st = s_state[r];
+          const float m = fmaxf(m_used, st.x);
+          const float ref = m == -INFINITY ? 0.f : m;
+          f0 = fast_exp2(m_used - ref);
+          f1 = fast_exp2(st.x - ref);
+          l = l * f0 + st.y * f1;
+          m_used = m;
+        }
+        if (n_other > 0) ++uses[1 - x];
+      }
+      if (n_x > 0) tc_fence_after_sync();
       // A query tile whose tokens see none of the segment's tiles (n_x = 0)
       // still owes its part of a shared block: o = 0, lse = -inf.
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * kLn2;
+      f0 *= inv;
+      f1 *= inv;
       const int h = kvh * a.group + r % a.group;
       const int64_t orow = static_cast<int64_t>(valid ? sg.b.t_base + tok : 0) * a.hq + h;
       constexpr int kRows = kQT * kM;
       const int64_t part = static_cast<int64_t>(sg.slot) * a.hkv + kvh;
-      float4 *po = reinterpret_cast<float4 *>(a.part_o) + part * (D / 4) * kRows + x * kM + r;
+      float4 *po = reinterpret_cast<float4 *>(a.part_o) + part * (D / 4) * kRows + xq * kM + r;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
         float o[32];
         if (n_x > 0) {
           tmem_ld32(orow_t + cb * 32, o);
-          tmem_ld_wait();
+          if (shared) {
+            float o1[32];
+            tmem_ld32(orow_t + kN + cb * 32, o1);
+            tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] *= inv;
+            for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + o1[q] * f1;
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] *= f0;
+          }
         } else {
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = 0.f;
@@ -787,13 +891,14 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       }
       if (valid) {
         if (!sg.whole)
-          a.part_lse[part * kRows + x * kM + r] = lse;
+          a.part_lse[part * kRows + xq * kM + r] = lse;
         else if (a.lse)
           a.lse[orow] = lse;
       }
       if (n_x > 0) {
         tc_fence_before_sync();
         mbar_arrive(bar(kBarOEmpty + x));
+        if (shared) mbar_arrive(bar(kBarOEmpty + 1));
       }
     }
     if (!ok) {
@@ -817,63 +922,86 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
 }
 
 // Merge of the blocks that more than one group computed: o = sum e^(lse_s -
-// lse) o_s. One CTA per (block, kv head, 32 rows); lane = row, so the states'
-// [column group][row] layout is read in whole lines.
+// lse) o_s. One CTA per (block, kv head, 32 rows), eight warps with D / 8
+// columns each; lane = row, so the states' [column group][row] layout is read
+// in whole lines. States are taken kBatch at a time, all their loads together,
+// with a running maximum: one round trip to L2 for the usual two or three.
+constexpr int kMergeThreads = 256;
+
 template <int D, int kQT>
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
   constexpr int kRows = kQT * kM;
-  grid_dependency_wait();
+  constexpr int kCols = D / 4 / (kMergeThreads / 32);  // float4 columns per warp
+  constexpr int kBatch = 4;
   const int b = blockIdx.x;
+  // inputs of the call, complete before any CTA of tree_kernel went on
+  const Block k = load_block<kQT>(a, b, false);
+  grid_dependency_wait();
   const int2 e = a.table[b];
   if (e.x < 0) return;
-  const Block k = load_block<kQT>(a, b, false);
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int kvh = blockIdx.y;
   const int row = blockIdx.z * kMergeRows + lane;  // of the block's query tiles
   const int tt = (row % kM) / a.group;
   const int tok = (row / kM) * a.tokens_per_tile + tt;
-  const bool valid = tt < a.tokens_per_tile && tok < k.tokens;
-  // segment s: the block's first one, then slot 2 g of each further group
-  const int n = e.y - (e.x >> 1) + 1;
-  auto part = [&](int s) -> int64_t {
-    return static_cast<int64_t>(s == 0 ? e.x : 2 * ((e.x >> 1) + s)) * a.hkv + kvh;
-  };
-  if (!valid) return;
+  if (tt >= a.tokens_per_tile || tok >= k.tokens) return;
+  // state s: slot 2 g + 1 of the block's first group, then 2 g of each further one
+  const int n = e.y - e.x + 1;
   float m = -INFINITY, l = 0.f;
-  for (int s = 0; s < n; ++s) {
-    m = fmaxf(m, a.part_lse[part(s) * kRows + row]);
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
-  constexpr int kPer = D / 4 / 4;  // column groups per warp
-  float4 o[kPer];
+  float4 o[kCols];
 #pragma unroll
-  for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < n; ++s) {
-    const float w = expf(a.part_lse[part(s) * kRows + row] - ref);
-    l += w;
-    const float4 *po = reinterpret_cast<const float4 *>(a.part_o) + part(s) * (D / 4) * kRows +
-                       static_cast<int64_t>(warp * kPer) * kRows + row;
-    float4 v[kPer];
+  for (int c = 0; c < kCols; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += kBatch) {
+    float lse[kBatch];
+    float4 v[kBatch][kCols];
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) v[c] = po[c * kRows];
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = s0 + u;
+      const int64_t part = static_cast<int64_t>(2 * (e.x + s) + (s == 0 ? 1 : 0)) * a.hkv + kvh;
+      const float4 *po = reinterpret_cast<const float4 *>(a.part_o) + part * (D / 4) * kRows +
+                         static_cast<int64_t>(warp * kCols) * kRows + row;
+      lse[u] = s < n ? a.part_lse[part * kRows + row] : -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      o[c].x += w * v[c].x;
-      o[c].y += w * v[c].y;
-      o[c].z += w * v[c].z;
-      o[c].w += w * v[c].w;
+      for (int c = 0; c < kCols; ++c)
+        v[u][c] = s < n ? po[c * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) mx = fmaxf(mx, lse[u]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float f = expf(m - ref);
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      o[c].x *= f;
+      o[c].y *= f;
+      o[c].z *= f;
+      o[c].w *= f;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float w = expf(lse[u] - ref);
+      l += w;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        o[c].x += w * v[u][c].x;
+        o[c].y += w * v[u][c].y;
+        o[c].z += w * v[u][c].z;
+        o[c].w += w * v[u][c].w;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t orow =
       static_cast<int64_t>(k.t_base + tok) * a.hq + kvh * a.group + (row % kM) % a.group;
-  uint2 *dst = reinterpret_cast<uint2 *>(a.o + orow * D) + warp * kPer;
+  uint2 *dst = reinterpret_cast<uint2 *>(a.o + orow * D) + warp * kCols;
 #pragma unroll
-  for (int c = 0; c < kPer; ++c)
+  for (int c = 0; c < kCols; ++c)
     dst[c] = make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv),
                         pack_bf16(o[c].z * inv, o[c].w * inv));
-  if (warp == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : ref + logf(l);
+  if (warp == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 template <int D, int kQT, bool kTma>
@@ -887,7 +1015,7 @@ cudaError_t launch(const TreeArgs &a, const CUtensorMap &km, const CUtensorMap &
   e = launch_pdl(tree_kernel<D, kQT, kTma>, grid, block, S::kTotal, stream, km, vm, qm, a);
   if (e != cudaSuccess || a.groups == 1) return e;
   const dim3 mgrid(a.batch * a.blocks_per_req, a.hkv, kQT * kM / kMergeRows);
-  return launch_pdl(tree_merge_kernel<D, kQT>, mgrid, dim3(128), 0, stream, a);
+  return launch_pdl(tree_merge_kernel<D, kQT>, mgrid, dim3(kMergeThreads), 0, stream, a);
 }
 
 template <int D>
