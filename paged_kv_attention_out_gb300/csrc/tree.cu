@@ -31,7 +31,8 @@
 //       alternately into a ring of slots; kTma: three warps, TMA boxes of a
 //       power of two of rows that divides the page size, the box holding the
 //       request's last key by 16-byte cp.async with zero fill, so that no
-//       stale bits behind it reach P V; otherwise two or four warps of cp.async.
+//       stale bits behind it reach P V; otherwise three or four warps of
+//       cp.async.
 // With one query tile the scores are double buffered, S(j + 1) is computed
 // while the softmax works on S(j); with two, the tiles take turns. A block of
 // the two-tile kernel whose tokens fit one tile is walked by both softmax
@@ -70,13 +71,14 @@ constexpr int kMinTiles = 2;  // smallest share of a group: two key tiles
 constexpr int kCost1 = PKV_TREE_COST1, kCost2 = PKV_TREE_COST2;
 constexpr int kMergeRows = 32;
 
-// Producer warps: with two query tiles the CTA's twelfth warp is the last that
-// costs no registers (a softmax thread holds a whole score row). By TMA each
-// warp issues every third K or V tile: a warp's issue of boxes of 16 rows, one
-// lane after the other, takes longer than their bytes do (page size 16, one
-// query tile: 185 us with one warp).
+// Producer warps; warp w issues every kProducerWarps-th K or V tile. A warp
+// takes longer to issue a tile's copies than their bytes take (boxes of 16
+// rows one lane after the other, or 64 row pieces per lane), so several work
+// at a time: twelve warps of a CTA cost no more registers than ten (a softmax
+// thread holds a whole score row). Page size 16, one query tile: 185 us with
+// one TMA warp, 147 with three.
 constexpr int producer_warps(int query_tiles, bool tma) {
-  return tma ? 3 : (query_tiles == 2 ? 2 : 4);
+  return tma || query_tiles == 2 ? 3 : 4;
 }
 
 template <int D, int kQT>
@@ -92,6 +94,12 @@ struct TreeSmem {
   static constexpr int kTotal = kBars + 32 * 8 + 1024;
   static_assert(kTotal <= 227 * 1024 - 1792, "shared memory (with the static arrays)");
   static_assert(kTotal > 114 * 1024, "one CTA per SM");
+  // A warp that waits for unit u's slot has issued unit u - warps, so unit u -
+  // warps - slots is consumed, and with it every unit up to two before it (K
+  // tiles are consumed ahead of the V tile before them): unit u - 2 slots among
+  // them, without which the parity waited for could be an older phase's.
+  static_assert(producer_warps(kQT, true) <= kSlots - 2 && producer_warps(kQT, false) <= kSlots - 2,
+                "producer warps run too far ahead of the ring");
 };
 
 enum : int {
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kBarFull + i), (kTma ? 1 : kProducerWarps) * 32);
+      mbar_init(bar(kBarFull + i), 32);  // the lanes of the warp that fills it
       mbar_init(bar(kBarEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -387,23 +395,24 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     // first (page size 64: 144.7 us against 150.2 with the default policy).
     const uint64_t kv_policy = a.blocks_per_req == 1 ? l2_evict_first_policy()
                                                      : l2_evict_normal_policy();
-    constexpr int kGroups = kTma ? 1 : kN / (32 * kProducerWarps);  // keys per lane and tile
+    constexpr int kGroups = kTma ? 1 : kN / 32;  // boxes (keys) per lane and tile
     constexpr int kChunks = D / 8;
     constexpr int kKeysPerInstr = 32 / kChunks;
     const int ch = lane % kChunks;
     bool ok = true;
-    uint32_t u = 0;  // ring units (K and V tiles) issued
+    uint32_t u0 = 0;  // ring unit (K and V tiles) of the segment's first tile
+    uint32_t issued = 0;  // one past this warp's last unit
     int segs = 0;
     while (ok && next_segment<kQT>(a, walk, sg)) {
       const int row = a.table_idx ? a.table_idx[sg.b.req] : sg.b.req;
       const int32_t *pages = a.page_table + static_cast<int64_t>(row) * a.table_stride;
       // This lane's boxes of tile j (kTma: box `lane` of the tile; otherwise
-      // one key of each 32 the warp copies): the page entry, loaded a tile
+      // one key of each 32): the page entry, loaded one of the warp's units
       // ahead and looked at only when the tile's copies are issued, and the
       // first pool row (-1 past the request or for a bad page).
       const int box = kTma ? a.box : 1;
       auto box_key = [&](int j, int g) -> int {
-        const int at = kTma ? lane * box : (pw * kGroups + g) * 32 + lane;
+        const int at = kTma ? lane * box : g * 32 + lane;
         const int key = (sg.tile0 + j) * kN + at;
         return at < kN && key < sg.b.seq ? key : -1;
       };
@@ -424,8 +433,13 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         }
         return s;
       };
+      // this warp's units of the segment: first, first + kProducerWarps, ..
+      // (unit w holds K, or V if w is odd, of tile w / 2)
+      const uint32_t n_units = 2u * static_cast<uint32_t>(sg.n);
+      const uint32_t first =
+          (static_cast<uint32_t>(pw) + kProducerWarps - u0 % kProducerWarps) % kProducerWarps;
       int next[kGroups];
-      load_entries(0, next);
+      if (first < n_units) load_entries(static_cast<int>(first >> 1), next);
       if (pw == 0) {
         if (segs > 0) ok = mbar_wait_warp(bar(kBarQEmpty), (segs - 1) & 1, abort);
         if (ok && lane == 0) {
@@ -443,66 +457,86 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         if (!ok) break;
       }
       ++segs;
-      for (int j = 0; ok && j < sg.n; ++j) {
+      for (uint32_t w = first; w < n_units; w += kProducerWarps) {
+        const int j = static_cast<int>(w >> 1), c = static_cast<int>(w & 1);
+        const uint32_t u = u0 + w;
         const int key0 = (sg.tile0 + j) * kN;
         long long cur[kGroups];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) cur[g] = first_row(j, g, next[g]);
-        if (j + 1 < sg.n) load_entries(j + 1, next);
+        if (w + kProducerWarps < n_units)
+          load_entries(static_cast<int>((w + kProducerWarps) >> 1), next);
+        const int st = static_cast<int>(u % kSlots);
+        if (u >= kSlots &&
+            !(ok = mbar_wait_warp(bar(kBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
+          break;
+        const uint32_t dst = sbase + S::kRing + st * S::kSlotBytes;
+        const __nv_bfloat16 *plane = (c ? a.v_plane : a.k_plane) + head_off;
+        if (kTma) {
+          // boxes of live keys by TMA; the box of the last key and those
+          // behind it (and bad pages) row by row, zeros where nothing is
+          const int b_lane = lane * box;
+          const bool in_tile = b_lane < kN;
+          const bool live = in_tile && cur[0] >= 0 && key0 + b_lane + box <= sg.b.seq;
+          const unsigned live_mask = __ballot_sync(0xffffffffu, live);
+          unsigned rest = __ballot_sync(0xffffffffu, in_tile && !live);
+          if (lane == 0)
+            mbar_expect_tx(bar(kBarFull + st),
+                           static_cast<uint32_t>(__popc(live_mask) * box * D * 2));
+          __syncwarp();
+          if (live) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c, ++u) {
-          if (kTma && u % kProducerWarps != static_cast<uint32_t>(pw)) continue;
-          const int st = static_cast<int>(u % kSlots);
-          if (u >= kSlots &&
-              !(ok = mbar_wait_warp(bar(kBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
-            break;
-          const uint32_t dst = sbase + S::kRing + st * S::kSlotBytes;
-          const __nv_bfloat16 *plane = (c ? a.v_plane : a.k_plane) + head_off;
-          if (kTma) {
-            // boxes of live keys by TMA; the box of the last key and those
-            // behind it (and bad pages) row by row, zeros where nothing is
-            const int b_lane = lane * box;
-            const bool in_tile = b_lane < kN;
-            const bool live = in_tile && cur[0] >= 0 && key0 + b_lane + box <= sg.b.seq;
-            const unsigned live_mask = __ballot_sync(0xffffffffu, live);
-            unsigned rest = __ballot_sync(0xffffffffu, in_tile && !live);
-            if (lane == 0)
-              mbar_expect_tx(bar(kBarFull + st),
-                             static_cast<uint32_t>(__popc(live_mask) * box * D * 2));
-            __syncwarp();
-            if (live) {
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h)
-                tma_load_2d_hint(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
-                                 c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
-                                 bar(kBarFull + st), kv_policy);
-            }
-            while (rest) {
-              const int src = __ffs(rest) - 1;
-              rest &= rest - 1;
-              const long long s0 = __shfl_sync(0xffffffffu, cur[0], src);
-              for (int r = lane / kChunks; r < box; r += kKeysPerInstr) {
-                const int kk = src * box + r;
-                const bool in = s0 >= 0 && key0 + kk < sg.b.seq;
-                cp_async_16(dst + sw128_offset(kN, kk, ch * 8),
-                            in ? plane + (s0 + r) * row_elems + ch * 8 : plane, in ? 16 : 0);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-#pragma unroll 4
-              for (int it = 0; it < 32 / kKeysPerInstr; ++it) {
-                const int kl = it * kKeysPerInstr + lane / kChunks;
-                const long long s0 = __shfl_sync(0xffffffffu, cur[g], kl);
-                cp_async_16_hint(dst + sw128_offset(kN, (pw * kGroups + g) * 32 + kl, ch * 8),
-                                 s0 >= 0 ? plane + s0 * row_elems + ch * 8 : plane,
-                                 s0 >= 0 ? 16 : 0, kv_policy);
-              }
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_2d_hint(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
+                               c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
+                               bar(kBarFull + st), kv_policy);
           }
-          cp_async_mbar_arrive(bar(kBarFull + st));
+          while (rest) {
+            const int src = __ffs(rest) - 1;
+            rest &= rest - 1;
+            const long long s0 = __shfl_sync(0xffffffffu, cur[0], src);
+            for (int r = lane / kChunks; r < box; r += kKeysPerInstr) {
+              const int kk = src * box + r;
+              const bool in = s0 >= 0 && key0 + kk < sg.b.seq;
+              cp_async_16(dst + sw128_offset(kN, kk, ch * 8),
+                          in ? plane + (s0 + r) * row_elems + ch * 8 : plane, in ? 16 : 0);
+            }
+          }
+        } else {
+          // A lane knows the rows of four of the tile's keys; each copy takes
+          // its row's address from the lane that does. Eight addresses are
+          // exchanged before their copies: a copy keeps its place in the
+          // program, a shuffle between two would delay the second.
+          constexpr int kCopies = 32 / kKeysPerInstr;
+          constexpr int kAhead = 8;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const bool in = cur[g] >= 0;
+            const unsigned mask = __ballot_sync(0xffffffffu, in) >> (lane / kChunks);
+            const uint64_t row_at =
+                reinterpret_cast<uint64_t>(in ? plane + cur[g] * row_elems : plane);
+#pragma unroll
+            for (int i0 = 0; i0 < kCopies; i0 += kAhead) {
+              uint64_t src[kAhead];
+#pragma unroll
+              for (int i = 0; i < kAhead; ++i)
+                src[i] = __shfl_sync(0xffffffffu, row_at,
+                                     (i0 + i) * kKeysPerInstr + lane / kChunks) +
+                         ch * 16;
+#pragma unroll
+              for (int i = 0; i < kAhead; ++i)
+                cp_async_16_hint(
+                    dst + sw128_offset(kN, g * 32 + (i0 + i) * kKeysPerInstr + lane / kChunks,
+                                       ch * 8),
+                    reinterpret_cast<const void *>(src[i]),
+                    (mask >> ((i0 + i) * kKeysPerInstr)) & 1u ? 16 : 0, kv_policy);
+            }
+          }
         }
+        cp_async_mbar_arrive(bar(kBarFull + st));
+        issued = u + 1;
       }
+      u0 += n_units;
     }
     if (!ok) *abort = 1;
     cp_async_wait_all();
@@ -511,7 +545,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       int never = 0;
       if (pw == 0 && segs > 0) mbar_wait(bar(kBarQFull), (segs - 1) & 1, &never);
       if (kTma)
-        for (uint32_t t = u > kSlots ? u - kSlots : 0; t < u; ++t)
+        for (uint32_t t = issued > kSlots ? issued - kSlots : 0; t < issued; ++t)
           if (t % kProducerWarps == static_cast<uint32_t>(pw))
             mbar_wait(bar(kBarFull + t % kSlots), (t / kSlots) & 1, &never);
     }
