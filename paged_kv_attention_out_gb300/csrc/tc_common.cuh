@@ -334,6 +334,32 @@ __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, vo
   }
 }
 
+// The same for a whole warp that stays together (the result is uniform, the
+// code after it may be issued by an elected lane). The abort flag and the clock
+// are looked at from the 32nd failed test on: either costs more than the usual
+// wait of a warp that issues MMAs.
+__device__ __forceinline__ bool mbar_wait_uniform(uint32_t bar, uint32_t parity,
+                                                  volatile int *abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if ((i & 31) == 31) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > 2000000000ull)) return false;
+    }
+  }
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 // mbar_wait by every lane of a warp, with a warp-uniform result: code after
 // it may use .sync.aligned instructions (tcgen05.ld/st) safely.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {

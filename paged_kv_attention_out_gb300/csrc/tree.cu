@@ -26,7 +26,10 @@
 //
 // Roles of a CTA (kQT = 1 or 2 query tiles of 128 rows):
 //   warps 0 .. 4 kQT - 1  softmax: one query row per thread (TMEM lane)
-//   next warp             TMEM allocation and the single MMA-issuing thread
+//   next warp             TMEM allocation and the MMAs. The warp stays together
+//       and one elected lane issues, so that descriptors and loop state are in
+//       uniform registers: a lone thread took 60 clocks an MMA or commit, which
+//       made this warp the bound.
 //   the rest              producers: the Q tiles by TMA, then K and V tiles
 //       alternately into a ring of slots; kTma: three warps, TMA boxes of a
 //       power of two of rows that divides the page size, the box holding the
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   __shared__ float2 s_state[kQT == 2 ? kM : 1];  // (m, l) of group 1's rows (shared query tile)
   __shared__ uint8_t s_parents[kQT][kMaxTree];  // a copy for each softmax group; root: 255
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform for the compiler, too)
   const int lane = tid & 31;
   const int kvh = blockIdx.x;
   const int tpt = a.tokens_per_tile;
@@ -491,6 +494,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
                                c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
                                bar(kBarFull + st), kv_policy);
           }
+          const bool copied = rest != 0;
           while (rest) {
             const int src = __ffs(rest) - 1;
             rest &= rest - 1;
@@ -502,6 +506,11 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
                           in ? plane + (s0 + r) * row_elems + ch * 8 : plane, in ? 16 : 0);
             }
           }
+          if (copied) {  // landed, and visible to tcgen05.mma, before the arrival
+            cp_async_wait_all();
+            fence_async_shared();
+          }
+          mbar_arrive(bar(kBarFull + st));
         } else {
           // A lane knows the rows of four of the tile's keys; each copy takes
           // its row's address from the lane that does. Eight addresses are
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
             }
           }
         }
-        cp_async_mbar_arrive(bar(kBarFull + st));
+        if (!kTma) cp_async_mbar_arrive(bar(kBarFull + st));
         issued = u + 1;
       }
       u0 += n_units;
@@ -551,137 +560,143 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
-      const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
-      const uint64_t dk0 = umma_desc_sw128(sbase + S::kRing, 16, 1024);
-      const uint64_t dv0 = umma_desc_sw128(sbase + S::kRing, kN * 128, 1024);
-      auto kstep = [](int ks) -> uint64_t {
-        return static_cast<uint64_t>(((ks >> 2) * (kN * 128) + (ks & 3) * 32) >> 4);
-      };
-      auto slot_step = [](uint32_t u) -> uint64_t {
-        return static_cast<uint64_t>((u % kSlots) * (S::kSlotBytes >> 4));
-      };
-      auto qk = [&](int x, int buf, uint32_t u) {  // scores of query tile x, K in unit u
-        const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
-        const uint64_t dk = dk0 + slot_step(u);
+    const bool issuer = elect_one();
+    constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
+    constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
+    const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
+    const uint64_t dk0 = umma_desc_sw128(sbase + S::kRing, 16, 1024);
+    const uint64_t dv0 = umma_desc_sw128(sbase + S::kRing, kN * 128, 1024);
+    auto kstep = [](int ks) -> uint64_t {
+      return static_cast<uint64_t>(((ks >> 2) * (kN * 128) + (ks & 3) * 32) >> 4);
+    };
+    auto slot_step = [](uint32_t u) -> uint64_t {
+      return static_cast<uint64_t>((u % kSlots) * (S::kSlotBytes >> 4));
+    };
+    auto qk = [&](int x, int buf, uint32_t u) {  // scores of query tile x, K in unit u
+      const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
+      const uint64_t dk = dk0 + slot_step(u);
+      if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           umma_bf16_ss(tmem + kTmemS + buf * kN, dq + kstep(ks), dk + kstep(ks), idesc_qk,
                        ks > 0 ? 1u : 0u);
         umma_commit(bar(kBarSFull + buf));
-      };
-      auto pv = [&](int x, int buf, uint32_t u, bool first) {  // O_x (+)= P V, V in unit u
-        const uint64_t dv = dv0 + slot_step(u);
+      }
+    };
+    auto pv = [&](int x, int buf, uint32_t u, bool first) {  // O_x (+)= P V, V in unit u
+      const uint64_t dv = dv0 + slot_step(u);
+      if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < kN / 16; ++ks)
           umma_bf16_ts(tmem + kTmemO + x * kN, tmem + kTmemS + buf * kN + ks * 8,
                        dv + ks * (2048 >> 4), idesc_pv, (!first || ks > 0) ? 1u : 0u);
-      };
-      auto wait_unit = [&](uint32_t u) {
-        const bool r = mbar_wait_fast(bar(kBarFull + u % kSlots), (u / kSlots) & 1, abort);
-        fence_async_shared();  // cp.async wrote (part of) it, tcgen05.mma reads it
-        tc_fence_after_sync();
-        return r;
-      };
-      auto free_unit = [&](uint32_t u) { umma_commit(bar(kBarEmpty + u % kSlots)); };
-      uint32_t u0 = 0;                // ring unit of the segment's first K tile
-      uint32_t np0 = 0, np1 = 0;      // P tiles taken from score buffers 0 and 1
-      uint32_t uses0 = 0, uses1 = 0;  // segments that used O_0, O_1
-      int segs = 0;
-      bool ok = true;
-      while (ok && next_segment<kQT>(a, walk, sg)) {
-        const int n = sg.n;
-        if (!(ok = mbar_wait_fast(bar(kBarQFull), segs & 1, abort))) break;
-        ++segs;
-        // One query tile: key tiles alternate between the score buffers, and
-        // (two-tile kernel) between the softmax groups and their O.
-        const bool alternate = kQT == 1 || shared_tile(a, sg);
-        if (alternate) {
-          for (int j = 0; ok && j < 2 && j < n; ++j) {
-            if (!(ok = wait_unit(u0 + 2 * j))) break;
-            qk(0, j, u0 + 2 * j);
-            free_unit(u0 + 2 * j);
-          }
-          if (n <= 2 && ok) umma_commit(bar(kBarQEmpty));
-          for (int j = 0; ok && j < n; ++j) {
-            const int buf = j & 1;
-            const int x = kQT == 2 ? buf : 0;
-            uint32_t &np = buf ? np1 : np0;
-            const uint32_t uses = x ? uses1 : uses0;
-            const bool first = j <= x;  // of O_x
-            if (first && uses > 0 &&
-                !(ok = mbar_wait_fast(bar(kBarOEmpty + x), (uses - 1) & 1, abort)))
-              break;
-            if (!(ok = mbar_wait_fast(bar(kBarPFull + buf), np & 1, abort) &&
-                       wait_unit(u0 + 2 * j + 1)))
-              break;
-            ++np;
-            pv(x, buf, u0 + 2 * j + 1, first);
-            free_unit(u0 + 2 * j + 1);
-            if (kQT == 1) umma_commit(bar(kBarPvDone));
-            if (kQT == 2 && j + 2 >= n) umma_commit(bar(kBarOFull + x));
-            if (j + 2 < n) {
-              if (!(ok = wait_unit(u0 + 2 * (j + 2)))) break;
-              qk(0, buf, u0 + 2 * (j + 2));
-              free_unit(u0 + 2 * (j + 2));
-              if (j + 3 == n) umma_commit(bar(kBarQEmpty));
-            }
-          }
-          if (kQT == 1 && ok) umma_commit(bar(kBarOFull));
-          ++uses0;
-          if (kQT == 2) ++uses1;
-        } else {
-          const int n0 = tiles_of(a, sg, tpb, 0), n1 = tiles_of(a, sg, tpb, 1);
-          // score tile j of both query tiles, for those that walk it
-          if (!(ok = wait_unit(u0))) break;
-          if (n0 > 0) qk(0, 0, u0);
-          if (n1 > 0) qk(1, 1, u0);
-          free_unit(u0);
-          if (n == 1) umma_commit(bar(kBarQEmpty));
-          for (int j = 0; ok && j < n; ++j) {
-            const uint32_t uk = u0 + 2 * (j + 1), uv = u0 + 2 * j + 1;
-            const bool next = j + 1 < n;
-            if (!(ok = wait_unit(uv))) break;
-            if (j < n0) {
-              if (j == 0 && uses0 > 0 &&
-                  !(ok = mbar_wait_fast(bar(kBarOEmpty), (uses0 - 1) & 1, abort)))
-                break;
-              if (!(ok = mbar_wait_fast(bar(kBarPFull), np0 & 1, abort))) break;
-              tc_fence_after_sync();
-              ++np0;
-              pv(0, 0, uv, j == 0);
-              if (j == n0 - 1) umma_commit(bar(kBarOFull));
-            }
-            if (next && !(ok = wait_unit(uk))) break;
-            if (next && j + 1 < n0) qk(0, 0, uk);
-            if (j < n1) {
-              if (j == 0 && uses1 > 0 &&
-                  !(ok = mbar_wait_fast(bar(kBarOEmpty + 1), (uses1 - 1) & 1, abort)))
-                break;
-              if (!(ok = mbar_wait_fast(bar(kBarPFull + 1), np1 & 1, abort))) break;
-              tc_fence_after_sync();
-              ++np1;
-              pv(1, 1, uv, j == 0);
-              if (j == n1 - 1) umma_commit(bar(kBarOFull + 1));
-            }
-            free_unit(uv);
-            if (next) {
-              if (j + 1 < n1) qk(1, 1, uk);
-              free_unit(uk);
-            }
-            if (j + 2 == n) umma_commit(bar(kBarQEmpty));
-          }
-          if (n0 > 0) ++uses0;
-          if (n1 > 0) ++uses1;
+      }
+    };
+    auto commit = [&](int i) {
+      if (issuer) umma_commit(bar(i));
+    };
+    auto wait_unit = [&](uint32_t u) {
+      const bool r = mbar_wait_uniform(bar(kBarFull + u % kSlots), (u / kSlots) & 1, abort);
+      if (!kTma) fence_async_shared();  // cp.async wrote it, tcgen05.mma reads it
+      tc_fence_after_sync();
+      return r;
+    };
+    auto free_unit = [&](uint32_t u) { commit(kBarEmpty + static_cast<int>(u % kSlots)); };
+    uint32_t u0 = 0;                // ring unit of the segment's first K tile
+    uint32_t np0 = 0, np1 = 0;      // P tiles taken from score buffers 0 and 1
+    uint32_t uses0 = 0, uses1 = 0;  // segments that used O_0, O_1
+    int segs = 0;
+    bool ok = true;
+    while (ok && next_segment<kQT>(a, walk, sg)) {
+      const int n = sg.n;
+      if (!(ok = mbar_wait_uniform(bar(kBarQFull), segs & 1, abort))) break;
+      ++segs;
+      // One query tile: key tiles alternate between the score buffers, and
+      // (two-tile kernel) between the softmax groups and their O.
+      const bool alternate = kQT == 1 || shared_tile(a, sg);
+      if (alternate) {
+        for (int j = 0; ok && j < 2 && j < n; ++j) {
+          if (!(ok = wait_unit(u0 + 2 * j))) break;
+          qk(0, j, u0 + 2 * j);
+          free_unit(u0 + 2 * j);
         }
-        u0 += 2 * static_cast<uint32_t>(n);
+        if (n <= 2 && ok) commit(kBarQEmpty);
+        for (int j = 0; ok && j < n; ++j) {
+          const int buf = j & 1;
+          const int x = kQT == 2 ? buf : 0;
+          uint32_t &np = buf ? np1 : np0;
+          const uint32_t uses = x ? uses1 : uses0;
+          const bool first = j <= x;  // of O_x
+          if (first && uses > 0 &&
+              !(ok = mbar_wait_uniform(bar(kBarOEmpty + x), (uses - 1) & 1, abort)))
+            break;
+          if (!(ok = mbar_wait_uniform(bar(kBarPFull + buf), np & 1, abort) &&
+                     wait_unit(u0 + 2 * j + 1)))
+            break;
+          ++np;
+          pv(x, buf, u0 + 2 * j + 1, first);
+          free_unit(u0 + 2 * j + 1);
+          if (kQT == 1) commit(kBarPvDone);
+          if (kQT == 2 && j + 2 >= n) commit(kBarOFull + x);
+          if (j + 2 < n) {
+            if (!(ok = wait_unit(u0 + 2 * (j + 2)))) break;
+            qk(0, buf, u0 + 2 * (j + 2));
+            free_unit(u0 + 2 * (j + 2));
+            if (j + 3 == n) commit(kBarQEmpty);
+          }
+        }
+        if (kQT == 1 && ok) commit(kBarOFull);
+        ++uses0;
+        if (kQT == 2) ++uses1;
+      } else {
+        const int n0 = tiles_of(a, sg, tpb, 0), n1 = tiles_of(a, sg, tpb, 1);
+        // score tile j of both query tiles, for those that walk it
+        if (!(ok = wait_unit(u0))) break;
+        if (n0 > 0) qk(0, 0, u0);
+        if (n1 > 0) qk(1, 1, u0);
+        free_unit(u0);
+        if (n == 1) commit(kBarQEmpty);
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t uk = u0 + 2 * (j + 1), uv = u0 + 2 * j + 1;
+          const bool next = j + 1 < n;
+          if (!(ok = wait_unit(uv))) break;
+          if (j < n0) {
+            if (j == 0 && uses0 > 0 &&
+                !(ok = mbar_wait_uniform(bar(kBarOEmpty), (uses0 - 1) & 1, abort)))
+              break;
+            if (!(ok = mbar_wait_uniform(bar(kBarPFull), np0 & 1, abort))) break;
+            tc_fence_after_sync();
+            ++np0;
+            pv(0, 0, uv, j == 0);
+            if (j == n0 - 1) commit(kBarOFull);
+          }
+          if (next && !(ok = wait_unit(uk))) break;
+          if (next && j + 1 < n0) qk(0, 0, uk);
+          if (j < n1) {
+            if (j == 0 && uses1 > 0 &&
+                !(ok = mbar_wait_uniform(bar(kBarOEmpty + 1), (uses1 - 1) & 1, abort)))
+              break;
+            if (!(ok = mbar_wait_uniform(bar(kBarPFull + 1), np1 & 1, abort))) break;
+            tc_fence_after_sync();
+            ++np1;
+            pv(1, 1, uv, j == 0);
+            if (j == n1 - 1) commit(kBarOFull + 1);
+          }
+          free_unit(uv);
+          if (next) {
+            if (j + 1 < n1) qk(1, 1, uk);
+            free_unit(uk);
+          }
+          if (j + 2 == n) commit(kBarQEmpty);
+        }
+        if (n0 > 0) ++uses0;
+        if (n1 > 0) ++uses1;
       }
-      if (!ok) {
-        *abort = 1;
-        flag_error(a.err, kErrTimeout);
-      }
+      u0 += 2 * static_cast<uint32_t>(n);
+    }
+    if (!ok) {
+      *abort = 1;
+      flag_error(a.err, kErrTimeout);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -942,10 +957,13 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   }
 
   // Teardown: every role has left its loop; free TMEM once no MMA is in flight.
-  if (warp == kMmaWarp && lane == 0 && *abort) {
-    umma_commit(bar(kBarTeardown));
-    int never = 0;
-    mbar_wait(bar(kBarTeardown), 0, &never);
+  if (warp == kMmaWarp && __any_sync(0xffffffffu, *abort != 0)) {
+    if (elect_one()) {  // the lane that issued them
+      umma_commit(bar(kBarTeardown));
+      int never = 0;
+      mbar_wait(bar(kBarTeardown), 0, &never);
+    }
+    __syncwarp();
   }
   tc_fence_before_sync();
   __syncthreads();
