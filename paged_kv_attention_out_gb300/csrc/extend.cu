@@ -40,7 +40,10 @@
 //              rescaled only when a row max grows by more than 2^8), masks
 //              only on tiles that cross some row's last key; then O / l ->
 //              bf16 and lse.
-//   warp 8     TMEM allocation and the single MMA-issuing thread.
+//   warp 8     TMEM allocation and the MMAs, issued by one elected lane of the
+//              warp, which stays together (a lone thread takes about 60
+//              clocks an MMA or commit, and the MMAs of a pair of tiles are
+//              the bound then).
 //   warp 9     producer: takes the work items, then per item the Q tiles
 //              (3-D TMA boxes) and the K and V tiles (2-D TMA boxes of 128
 //              keys x 64 columns, 128-byte swizzle) into two stages; a stage
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tile (kept here, not in registers, across the warp's key-tile loop).
   __shared__ int s_sm_state[kSoftmaxWarps][3];
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform for the compiler, too)
   const int lane = tid & 31;
   const int tpt = a.tokens_per_tile;
 
@@ -867,88 +870,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     // completed S_X(j+1) implies a completed PV_X(j) (O_X is then stable). Across items: the next item's S_X(0) may
     // run while softmax X writes the previous output (it only reads O_X);
     // its first PV_X waits until that output has been read out of O_X.
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
-      const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
-      const uint64_t dk0 = umma_desc_sw128(sbase + S::kKV, 16, 1024);
-      const uint64_t dv0 = umma_desc_sw128(sbase + S::kKV + S::kTileBytes, kN * 128, 1024);
-      constexpr uint64_t kStageStep = (2 * S::kTileBytes) >> 4;
-      auto kstep = [](int ks, int rows) -> uint64_t {
-        return static_cast<uint64_t>(((ks >> 2) * (rows * 128) + (ks & 3) * 32) >> 4);
-      };
-      auto qk = [&](int x, uint32_t gt) {  // S_x from CTA tile gt's K
-        const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
-        const uint64_t dk = dk0 + (gt & 1) * kStageStep;
+    const bool issuer = elect_one();
+    constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
+    constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
+    const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
+    const uint64_t dk0 = umma_desc_sw128(sbase + S::kKV, 16, 1024);
+    const uint64_t dv0 = umma_desc_sw128(sbase + S::kKV + S::kTileBytes, kN * 128, 1024);
+    constexpr uint64_t kStageStep = (2 * S::kTileBytes) >> 4;
+    auto kstep = [](int ks, int rows) -> uint64_t {
+      return static_cast<uint64_t>(((ks >> 2) * (rows * 128) + (ks & 3) * 32) >> 4);
+    };
+    auto qk = [&](int x, uint32_t gt) {  // S_x from CTA tile gt's K
+      const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
+      const uint64_t dk = dk0 + (gt & 1) * kStageStep;
+      if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           umma_bf16_ss(tmem + kTmemS + x * kN, dq + kstep(ks, kM), dk + kstep(ks, kN), idesc_qk,
                        ks > 0 ? 1u : 0u);
         umma_commit(bar(kPBarSFull + x));
-      };
-      // Per query tile (scalars): P V products issued and items that used
-      // the tile, over all items.
-      int pv_count0 = 0, pv_count1 = 0, uses0 = 0, uses1 = 0;
-      // O_x += P_x V(tile gt), j = the item's key tile; the item's first
-      // product overwrites O_x once the previous item's output is read out.
-      auto pv = [&](auto xc, int j, uint32_t gt) -> bool {
-        constexpr int x = decltype(xc)::value;
-        int &pv_count = x == 0 ? pv_count0 : pv_count1;
-        const int uses = x == 0 ? uses0 : uses1;
-        if (j == 0 && uses > 0 && !mbar_wait_fast(bar(kPBarOEmpty + x), (uses - 1) & 1, abort))
-          return false;
-        if (!mbar_wait_fast(bar(kPBarPFull + x), pv_count & 1, abort)) return false;
-        ++pv_count;
-        tc_fence_after_sync();
-        const uint64_t dv = dv0 + (gt & 1) * kStageStep;
+      }
+    };
+    auto commit = [&](int i) {
+      if (issuer) umma_commit(bar(i));
+    };
+    // Per query tile (scalars): P V products issued and items that used
+    // the tile, over all items.
+    int pv_count0 = 0, pv_count1 = 0, uses0 = 0, uses1 = 0;
+    // O_x += P_x V(tile gt), j = the item's key tile; the item's first
+    // product overwrites O_x once the previous item's output is read out.
+    auto pv = [&](auto xc, int j, uint32_t gt) -> bool {
+      constexpr int x = decltype(xc)::value;
+      int &pv_count = x == 0 ? pv_count0 : pv_count1;
+      const int uses = x == 0 ? uses0 : uses1;
+      if (j == 0 && uses > 0 && !mbar_wait_uniform(bar(kPBarOEmpty + x), (uses - 1) & 1, abort))
+        return false;
+      if (!mbar_wait_uniform(bar(kPBarPFull + x), pv_count & 1, abort)) return false;
+      ++pv_count;
+      tc_fence_after_sync();
+      const uint64_t dv = dv0 + (gt & 1) * kStageStep;
+      if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < kN / 16; ++ks)
           umma_bf16_ts(tmem + kTmemO + x * D, tmem + kTmemS + x * kN + ks * 8,
                        dv + ks * (2048 >> 4), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
-        return true;
-      };
-      uint32_t g = 0;  // K/V tiles consumed (all items)
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int slot = k & 1;
-        if (!(ok = mbar_wait_fast(bar(kPBarItemFull + slot), (k >> 1) & 1, abort))) break;
-        const Item d = s_item[slot];
-        mbar_arrive(bar(kPBarItemEmpty + slot));
-        if (d.req < 0) break;
-        const ItemGeom ig = item_geom(d, a);
-        const int n0 = ig.n0, n1 = ig.n1, n_tiles = ig.n_tiles;
-        const uint32_t g0 = g;
-        ok = mbar_wait_fast(bar(a.q_mode ? kPBarQReady : kPBarQFull), k & 1, abort) &&
-             mbar_wait_fast(bar(kPBarFull + (g0 & 1)), (g0 >> 1) & 1, abort);
+      }
+      return true;
+    };
+    uint32_t g = 0;  // K/V tiles consumed (all items)
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int slot = k & 1;
+      if (!(ok = mbar_wait_uniform(bar(kPBarItemFull + slot), (k >> 1) & 1, abort))) break;
+      const Item d = s_item[slot];
+      __syncwarp();
+      if (issuer) mbar_arrive(bar(kPBarItemEmpty + slot));
+      if (d.req < 0) break;
+      const ItemGeom ig = item_geom(d, a);
+      const int n0 = ig.n0, n1 = ig.n1, n_tiles = ig.n_tiles;
+      const uint32_t g0 = g;
+      ok = mbar_wait_uniform(bar(a.q_mode ? kPBarQReady : kPBarQFull), k & 1, abort) &&
+           mbar_wait_uniform(bar(kPBarFull + (g0 & 1)), (g0 >> 1) & 1, abort);
+      if (!ok) break;
+      tc_fence_after_sync();
+      qk(0, g0);
+      if (n1 > 0) qk(1, g0);
+      if (n_tiles == 1) commit(kPBarQEmpty);
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const uint32_t gj = g0 + static_cast<uint32_t>(j);
+        const bool next = j + 1 < n_tiles;
+        if (j < n0) ok = pv(kTile0, j, gj);
+        // O_0 is final once its last product is done (not held for tile 1's)
+        if (ok && j == n0 - 1) commit(kPBarOFull + 0);
+        if (ok && next) ok = mbar_wait_uniform(bar(kPBarFull + ((gj + 1) & 1)), ((gj + 1) >> 1) & 1, abort);
         if (!ok) break;
         tc_fence_after_sync();
-        qk(0, g0);
-        if (n1 > 0) qk(1, g0);
-        if (n_tiles == 1) umma_commit(bar(kPBarQEmpty));
-        for (int j = 0; j < n_tiles && ok; ++j) {
-          const uint32_t gj = g0 + static_cast<uint32_t>(j);
-          const bool next = j + 1 < n_tiles;
-          if (j < n0) ok = pv(kTile0, j, gj);
-          // O_0 is final once its last product is done (not held for tile 1's)
-          if (ok && j == n0 - 1) umma_commit(bar(kPBarOFull + 0));
-          if (ok && next) ok = mbar_wait_fast(bar(kPBarFull + ((gj + 1) & 1)), ((gj + 1) >> 1) & 1, abort);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (next && j + 1 < n0) qk(0, gj + 1);
-          if (j < n1 && !(ok = pv(kTile1, j, gj))) break;
-          if (j == n1 - 1) umma_commit(bar(kPBarOFull + 1));
-          umma_commit(bar(kPBarEmpty + (gj & 1)));
-          if (next && j + 1 < n1) qk(1, gj + 1);
-          if (j + 2 == n_tiles) umma_commit(bar(kPBarQEmpty));  // every S of the item issued
-        }
-        g = g0 + static_cast<uint32_t>(n_tiles);
-        ++uses0;
-        if (n1 > 0) ++uses1;
+        if (next && j + 1 < n0) qk(0, gj + 1);
+        if (j < n1 && !(ok = pv(kTile1, j, gj))) break;
+        if (j == n1 - 1) commit(kPBarOFull + 1);
+        commit(kPBarEmpty + static_cast<int>(gj & 1));
+        if (next && j + 1 < n1) qk(1, gj + 1);
+        if (j + 2 == n_tiles) commit(kPBarQEmpty);  // every S of the item issued
       }
-      if (!ok) {
-        *abort = 1;
-        flag_error(a.err, kErrTimeout);
-      }
+      g = g0 + static_cast<uint32_t>(n_tiles);
+      ++uses0;
+      if (n1 > 0) ++uses1;
+    }
+    if (!ok) {
+      *abort = 1;
+      flag_error(a.err, kErrTimeout);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -1170,10 +1180,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Teardown: every role has left its item loop (normally or through the
   // abort flag); free TMEM once no MMA is in flight.
-  if (warp == kMmaWarp && lane == 0 && *abort) {
-    umma_commit(bar(kPBarTeardown));  // tracks every MMA this thread issued
-    int never = 0;
-    mbar_wait(bar(kPBarTeardown), 0, &never);
+  if (warp == kMmaWarp && __any_sync(0xffffffffu, *abort != 0)) {
+    if (elect_one()) {
+      umma_commit(bar(kPBarTeardown));  // tracks every MMA this lane issued
+      int never = 0;
+      mbar_wait(bar(kPBarTeardown), 0, &never);
+    }
+    __syncwarp();
   }
   tc_fence_before_sync();
   __syncthreads();

@@ -64,14 +64,15 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxTree = PKV_MAX_TREE_TOKENS;
 constexpr int kMaskWords = kMaxTree / 32;
 constexpr int kMinTiles = 2;  // smallest share of a group: two key tiles
-// Cost of a key tile for a block of one and of two query tiles.
-#ifndef PKV_TREE_COST1
-#define PKV_TREE_COST1 3
-#endif
-#ifndef PKV_TREE_COST2
-#define PKV_TREE_COST2 5
-#endif
-constexpr int kCost1 = PKV_TREE_COST1, kCost2 = PKV_TREE_COST2;
+// Cost of a key tile for a block of one and of two query tiles. At D = 128
+// both are near the tile's 64 KB at the copy rate (64 drafts: 171, 170, 169 and
+// 176 us for 1:1, 5:6, 3:4 and 3:5; 33 drafts: 153, 155, 155 and 163); at 64
+// two tiles' softmax takes longer than 32 KB do (107, 117, 111 us for 3:5, 5:6
+// and 3:4; 33 drafts: 88, 106, 99).
+struct TileCost {
+  int one, two;
+};
+constexpr TileCost tile_cost(int d) { return d == 128 ? TileCost{5, 6} : TileCost{3, 5}; }
 constexpr int kMergeRows = 32;
 
 // Producer warps; warp w issues every kProducerWarps-th K or V tile. A warp
@@ -141,6 +142,7 @@ struct TreeArgs {
   int32_t max_tree;
   int32_t blocks_per_req;
   int32_t groups;
+  TileCost cost;
   int32_t box;           // rows of a K/V TMA box (kTma)
   float scale_log2;      // |scale| log2(e) (log2(e) for scale 0), > 0
   int32_t q_mode;        // 0: scores as they are, 1: negated (scale < 0), 2: zero (scale 0)
@@ -181,7 +183,7 @@ __device__ __forceinline__ Block load_block(const TreeArgs &a, int b, bool repor
   }
   k.t_base = beg + k.sub * tpb;
   k.tokens = min(tpb, k.c - k.sub * tpb);
-  k.cost = k.tokens <= a.tokens_per_tile ? kCost1 : kCost2;
+  k.cost = k.tokens <= a.tokens_per_tile ? a.cost.one : a.cost.two;
   k.tiles = k.tokens > 0 ? (k.p + k.sub * tpb + k.tokens + kN - 1) / kN : 0;
   return k;
 }
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       total += round;
     }
     // at least one tile begins in every share that a block covers
-    const long long per = max(static_cast<long long>(max(kMinTiles * kCost1, kCost2)),
+    const long long per = max(static_cast<long long>(max(kMinTiles * a.cost.one, a.cost.two)),
                               (total + a.groups - 1) / a.groups);
     const long long lo = per * blockIdx.y;
     const long long hi = min(total, lo + per);
@@ -749,6 +751,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
             if (i == 255) break;
           }
         }
+        __syncwarp();
       }
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; ok && j < n_x; ++j) {
@@ -922,21 +925,25 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
 #pragma unroll
           for (int q = 0; q < 32; ++q) o[q] = 0.f;
         }
-        if (!valid) continue;
-        if (sg.whole) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.o + orow * D + cb * 32);
+        if (valid) {
+          if (sg.whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.o + orow * D + cb * 32);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]),
-                                pack_bf16(o[8 * q + 2], o[8 * q + 3]),
-                                pack_bf16(o[8 * q + 4], o[8 * q + 5]),
-                                pack_bf16(o[8 * q + 6], o[8 * q + 7]));
-        } else {
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]),
+                                  pack_bf16(o[8 * q + 2], o[8 * q + 3]),
+                                  pack_bf16(o[8 * q + 4], o[8 * q + 5]),
+                                  pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+          } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            po[(cb * 8 + q) * kRows] =
-                make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 8; ++q)
+              po[(cb * 8 + q) * kRows] =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
         }
+        // tcgen05.ld wants the whole warp: without this barrier the compiler
+        // may split the loop by `valid` and issue it from part of one
+        __syncwarp();
       }
       if (valid) {
         if (!sg.whole)
@@ -1133,6 +1140,7 @@ cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const i
   a.max_tree = max_tree;
   a.blocks_per_req = plan.blocks_per_req;
   a.groups = plan.groups;
+  a.cost = tile_cost(g.d);
   a.q_mode = scale > 0.f ? 0 : (scale < 0.f ? 1 : 2);
   a.scale_log2 = scale > 0.f ? scale * kLog2e : (scale < 0.f ? -scale * kLog2e : kLog2e);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
