@@ -227,7 +227,7 @@ pkv_status pkv_paged_decode_attn_store(const pkv_pool *pool, int32_t layer, cons
  * plain causal rule.
  */
 typedef struct {
-  float soft_cap;              /* >= 0; 0: none                                */
+  float soft_cap;              /* 0: none; else > 0, |scale| / soft_cap <= 1e6 */
   const float *alibi_slopes;   /* device fp32 [num_q_heads], or NULL           */
   int32_t window;              /* >= 0; 0: none                                */
   const int32_t *prefix_lens;  /* device int32 [batch], clipped to 0 .. seq_len, or NULL */

@@ -46,8 +46,9 @@
 //              the bound then).
 //   warp 9     producer: takes the work items, then per item the Q tiles
 //              (3-D TMA boxes) and the K and V tiles (2-D TMA boxes of 128
-//              keys x 64 columns, 128-byte swizzle) into two stages; a stage
-//              is refilled once every MMA that reads it is done.
+//              keys x 64 columns, 128-byte swizzle) in turn into a ring of
+//              single tiles; a slot is refilled once every MMA that reads it
+//              is done.
 // Every hand-off is an mbarrier; every wait is bounded (tc_common.cuh).
 //
 // Score rules (a soft cap, a bias linear in the distance, a window, a prefix
@@ -86,12 +87,15 @@ struct Smem {
   static constexpr int kQ = 0;  // query tile X at kQ + X * kQBytes
   static constexpr int kQBytes = kM * D * 2;
   static constexpr int kTileBytes = kN * D * 2;
-  static constexpr int kKV = kQ + kQTiles * kQBytes;  // stage s: K at kKV + s*2*tile, V after it
-  static constexpr int kBars = kKV + 4 * kTileBytes;
-  // + alignment slack; never below 116 KB, so one CTA (and one 512-column
-  // TMEM allocation) per SM even for head_dim 64
-  static constexpr int kNeed = kBars + 32 * 8 + 1024;
-  static constexpr int kTotal = kNeed > 116 * 1024 ? kNeed : 116 * 1024;
+  static constexpr int kKV = kQ + kQTiles * kQBytes;  // slot s at kKV + s * tile
+  // K and V tiles take turns in a ring of single tiles, so a K tile's slot is
+  // loaded again as soon as its scores are done, not after the tile's P V.
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kBars = kKV + kSlots * kTileBytes;
+  // + alignment slack; above 114 KB, so one CTA (and one 512-column TMEM
+  // allocation) per SM even for head_dim 64
+  static constexpr int kTotal = kBars + 32 * 8 + 1024;
+  static_assert(kTotal > 114 * 1024 && kTotal <= 227 * 1024 - 512, "shared memory");
 };
 
 // TMEM columns: S_X (fp32 scores of query tile X) at 128 X, O_X at 256 + D X.
@@ -556,30 +560,30 @@ __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
 // pipeline described at the top, continued across items: the producer publishes the next
 // item (a two-slot descriptor ring) and loads its Q tiles as soon as every
 // S MMA of the current item is done, and its K/V tiles through the same
-// two-stage ring; the MMA thread issues the next item's first S while the
+// ring; the MMA warp issues the next item's first S while the
 // softmax warps write the current item's output, and its first P V once
 // they have read O. So a CTA's prologue (barrier setup, TMEM allocation,
 // the Q and first K/V loads) is paid once per SM, not once per block.
 // Every barrier keeps one phase sequence across items: tile counters for
-// the K/V stages and S/P hand-offs, item counters for the rest, counted per
+// the K/V ring and S/P hand-offs, item counters for the rest, counted per
 // query tile where a tile may sit out an item (no tokens), so a waiter is
 // never two phases behind (a barrier waited on with a parity completes at
 // most once between two waits of the same waiter).
 
 enum : int {
-  kPBarFull = 0,        // [2] producer: K and V tiles of stage s landed (TMA bytes)
-  kPBarEmpty = 2,       // [2] MMA: every MMA reading stage s done
-  kPBarSFull = 4,       // [2] MMA: S_X ready
-  kPBarPFull = 6,       // [2] softmax X: P_X in TMEM (and O_X rescaled)
-  kPBarOFull = 8,       // [2] MMA: every MMA of the item on query tile X done
-  kPBarOEmpty = 10,     // [2] softmax X: O_X read out (the item's output written)
-  kPBarItemFull = 12,   // [2] producer: descriptor slot written
-  kPBarItemEmpty = 14,  // [2] MMA thread + one lane per softmax warp: slot read
-  kPBarQFull = 16,      // producer: the item's Q tiles landed (TMA bytes)
-  kPBarQReady = 17,     // softmax warps: Q negated / zeroed in place (q_mode != 0)
-  kPBarQEmpty = 18,     // MMA: every S = Q K^T of the item done (Q may be reloaded)
-  kPBarTeardown = 19,   // MMA: everything issued has finished (abort path)
-  kPBarCount = 20,
+  kPBarFull = 0,        // [8] producer: the slot's K or V tile landed (TMA bytes)
+  kPBarEmpty = 8,       // [8] MMA: every MMA reading the slot done
+  kPBarSFull = 16,      // [2] MMA: S_X ready
+  kPBarPFull = 18,      // [2] softmax X: P_X in TMEM (and O_X rescaled)
+  kPBarOFull = 20,      // [2] MMA: every MMA of the item on query tile X done
+  kPBarOEmpty = 22,     // [2] softmax X: O_X read out (the item's output written)
+  kPBarItemFull = 24,   // [2] producer: descriptor slot written
+  kPBarItemEmpty = 26,  // [2] MMA warp + one lane per softmax warp: slot read
+  kPBarQFull = 28,      // producer: the item's Q tiles landed (TMA bytes)
+  kPBarQReady = 29,     // softmax warps: Q negated / zeroed in place (q_mode != 0)
+  kPBarQEmpty = 30,     // MMA: every S = Q K^T of the item done (Q may be reloaded)
+  kPBarTeardown = 31,   // MMA: everything issued has finished (abort path)
+  kPBarCount = 32,
 };
 static_assert(kPBarCount <= 32, "barrier area of Smem");
 
@@ -636,41 +640,31 @@ __device__ __forceinline__ Item shfl_desc(Item d) {
   return d;
 }
 
-// Capped scores in log2 units, in place: cap tanh(scale s / cap). Where every
-// score of the warp's rows is near zero against the cap, which the tile's
-// largest (mx*, from the loads) and smallest one tell, the polynomial runs on
-// the FMA pipe in pairs; the exponential form costs two more MUFU results per
-// score (ex2 and rcp beside the softmax's own ex2).
-__device__ __forceinline__ void cap_scores(float (&v)[kN], float mx0, float mx1, float mx2,
-                                           float mx3, const ScoreRules &rules) {
-  float lo = fminf(v[0], v[1]), lo1 = fminf(v[2], v[3]);
+// Score rules in the softmax. A tile is near if a bound of each row's scores
+// comes with the loads (the largest absolute raw score of each 32 columns
+// under a cap, the largest raw one under a bias alone), every raw score is in
+// the short polynomial's range, no column is masked and the bias is not so
+// steep that the bound would be far off. Its scores are then computed within
+// the exponential's argument, in pairs on the FMA pipe:
+//   y = s (c1 + u (c3 + u c5)) [+ slope cc] + (row terms - m),   u = s^2
+// three packed instructions more per pair for a cap, one for a bias, and the
+// reference m is that bound (at most 2 kNearLog2 + kNearBias above the row's
+// maximum, so nothing that counts underflows). Other tiles take the general
+// way: every score in place, masked, then its true maximum.
+constexpr float kNearBias = 46.f;  // most a bias may change within 32 columns, log2 units
+
+// All scores of a tile in log2 units, in place, without the bias.
+__device__ __forceinline__ void cap_scores(float (&v)[kN], float top, const ScoreRules &rules) {
+  if (__all_sync(0xffffffffu, top <= rules.near)) {
 #pragma unroll
-  for (int cc = 4; cc < kN; cc += 4) {
-    lo = min3f(lo, v[cc], v[cc + 1]);
-    lo1 = min3f(lo1, v[cc + 2], v[cc + 3]);
-  }
-  const float top = fmaxf(fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), -fminf(lo, lo1));
-  const bool far = !(top * rules.cap_in <= kTanhPoly);
-  if (__any_sync(0xffffffffu, far)) {
-#pragma unroll
-    for (int cc = 0; cc < kN; ++cc) v[cc] = rules.cap_log2 * rule_tanh(v[cc] * rules.cap_in);
-  } else {
-    // cap_log2 tanh(c s) = s (k1 + u (k3 + u (k5 + u (k7 + u k9)))), u = (c s)^2
-    const float k1 = rules.cap_log2 * rules.cap_in, k3 = k1 * kTanh3, k5 = k1 * kTanh5,
-                k7 = k1 * kTanh7, k9 = k1 * kTanh9;
-#pragma unroll
-    for (int cc = 0; cc < kN; cc += 2) {
-      const float2 s = make_float2(v[cc], v[cc + 1]);
-      const float2 x = __fmul2_rn(s, make_float2(rules.cap_in, rules.cap_in));
-      const float2 u = __fmul2_rn(x, x);
-      float2 p = __ffma2_rn(u, make_float2(k9, k9), make_float2(k7, k7));
-      p = __ffma2_rn(u, p, make_float2(k5, k5));
-      p = __ffma2_rn(u, p, make_float2(k3, k3));
-      p = __ffma2_rn(u, p, make_float2(k1, k1));
-      p = __fmul2_rn(s, p);
-      v[cc] = p.x;
-      v[cc + 1] = p.y;
+    for (int cc = 0; cc < kN; ++cc) {
+      const float u = v[cc] * v[cc];
+      v[cc] *= fmaf(u, fmaf(u, rules.c5, rules.c3), rules.c1);
     }
+  } else {
+#pragma unroll
+    for (int cc = 0; cc < kN; ++cc)
+      v[cc] = rules.cap_log2 * rule_tanh_far(v[cc] * rules.cap_in);
   }
 }
 
@@ -689,13 +683,8 @@ __device__ __forceinline__ float bias_scores(float (&v)[kN], float scale_log2, f
     return 0.f;
   }
 #pragma unroll
-  for (int cc = 0; cc < kN; cc += 2) {
-    float2 x = make_float2(v[cc], v[cc + 1]);
-    if (!kScaled) x = __fmul2_rn(x, make_float2(scale_log2, scale_log2));
-    x = __ffma2_rn(make_float2(slope, slope), make_float2(cc, cc + 1), x);
-    v[cc] = x.x;
-    v[cc + 1] = x.y;
-  }
+  for (int cc = 0; cc < kN; ++cc)
+    v[cc] = fmaf(slope, cc, kScaled ? v[cc] : v[cc] * scale_log2);
   return -slope * ft;
 }
 
@@ -707,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extend_tc_persistent_kernel(const __grid_constant__ CUtensorMap kv_map,
                                 const __grid_constant__ CUtensorMap q3_map, const Args a) {
   using S = Smem<D>;
+  constexpr int kSlots = S::kSlots;
   constexpr bool kRanges = (Args::kRules & kRuleRanges) != 0;
   constexpr bool kCap = (Args::kRules & kRuleCap) != 0;
   constexpr bool kBias = (Args::kRules & kRuleBias) != 0;
@@ -732,9 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Set-up that needs nothing from the gather kernel runs before the wait.
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(bar(kPBarFull + i), 1);  // the producer's expect_tx arrival
       mbar_init(bar(kPBarEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kPBarSFull + i), 1);
       mbar_init(bar(kPBarPFull + i), 128);  // the four warps of one query tile
       mbar_init(bar(kPBarOFull + i), 1);
@@ -773,9 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Per item: take the next item from the counter and publish it; once
     // every S of the previous item is done, load the item's two Q tiles
     // (lane l: rows 4 l .. 4 l + 3 of each, both 64-column halves; rows past
-    // the item's tokens read as zeros); then its K and V tiles, tile g of
-    // the CTA into stage g % 2 once every MMA reading that stage (tile
-    // g - 2) is done. Lane 0 issues the loads.
+    // the item's tokens read as zeros); then its K and V tiles, K of tile g
+    // of the CTA as ring unit 2 g and V as 2 g + 1, unit u into slot u %
+    // kSlots once every MMA reading that slot (unit u - kSlots) is done.
+    // Lane 0 issues the loads.
     constexpr int kHalves = D / 64;
     const uint64_t kv_policy = l2_evict_last_policy();
     const int total_items = a.hkv * a.plan[0];
@@ -783,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int *offs = a.plan + plan_offsets(a.nbuck, a.max_blocks);
     unsigned *counter = reinterpret_cast<unsigned *>(a.plan + 1);
     bool ok = true;
-    uint32_t g = 0;  // K/V tiles issued (all items)
+    uint32_t u = 0;  // ring units issued (all items)
     int q_loads = 0;
     for (int k = 0;; ++k) {
       const int slot = k & 1;
@@ -833,23 +826,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first workspace rows of this request's K and V runs for this kv head
       const int k_run = d.kvh * a.cap_rows + d.off;
       const int v_run = (a.hkv + d.kvh) * a.cap_rows + d.off;
-      for (int j = 0; j < ig.n_tiles; ++j, ++g) {
-        const int st = static_cast<int>(g & 1);
-        if (g >= 2 && !(ok = mbar_wait_warp(bar(kPBarEmpty + st), ((g >> 1) - 1) & 1, abort)))
-          break;
-        if (lane == 0) {
-          const uint32_t dst = sbase + S::kKV + st * 2 * S::kTileBytes;
-          mbar_arrive_expect_tx(bar(kPBarFull + st), 2 * S::kTileBytes);
-          const int tile = kRanges && j >= ig.walk.pre ? j + ig.walk.gap : j;
+      for (int j = 0; ok && j < ig.n_tiles; ++j) {
+        const int tile = kRanges && j >= ig.walk.pre ? j + ig.walk.gap : j;
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            tma_load_2d_hint(dst + h * (kN * 128), &kv_map, h * 64, k_run + tile * kN,
-                             bar(kPBarFull + st), kv_policy);
-            tma_load_2d_hint(dst + S::kTileBytes + h * (kN * 128), &kv_map, h * 64,
-                             v_run + tile * kN, bar(kPBarFull + st), kv_policy);
+        for (int c = 0; c < 2; ++c, ++u) {
+          const int st = static_cast<int>(u % kSlots);
+          if (u >= kSlots &&
+              !(ok = mbar_wait_warp(bar(kPBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
+            break;
+          if (lane == 0) {
+            const uint32_t dst = sbase + S::kKV + st * S::kTileBytes;
+            mbar_arrive_expect_tx(bar(kPBarFull + st), S::kTileBytes);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_2d_hint(dst + h * (kN * 128), &kv_map, h * 64,
+                               (c ? v_run : k_run) + tile * kN, bar(kPBarFull + st), kv_policy);
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!ok) break;
     }
@@ -859,8 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this CTA's shared memory need no other input to finish.
       int never = 0;
       if (q_loads > 0) mbar_wait(bar(kPBarQFull), (q_loads - 1) & 1, &never);
-      for (uint32_t t = g > 2 ? g - 2 : 0; t < g; ++t)
-        mbar_wait(bar(kPBarFull + (t & 1)), (t >> 1) & 1, &never);
+      for (uint32_t t = u > kSlots ? u - kSlots : 0; t < u; ++t)
+        mbar_wait(bar(kPBarFull + t % kSlots), (t / kSlots) & 1, &never);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -875,14 +869,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
     const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
     const uint64_t dk0 = umma_desc_sw128(sbase + S::kKV, 16, 1024);
-    const uint64_t dv0 = umma_desc_sw128(sbase + S::kKV + S::kTileBytes, kN * 128, 1024);
-    constexpr uint64_t kStageStep = (2 * S::kTileBytes) >> 4;
+    const uint64_t dv0 = umma_desc_sw128(sbase + S::kKV, kN * 128, 1024);
+    auto slot_step = [](uint32_t u) -> uint64_t {
+      return static_cast<uint64_t>((u % kSlots) * (S::kTileBytes >> 4));
+    };
     auto kstep = [](int ks, int rows) -> uint64_t {
       return static_cast<uint64_t>(((ks >> 2) * (rows * 128) + (ks & 3) * 32) >> 4);
     };
-    auto qk = [&](int x, uint32_t gt) {  // S_x from CTA tile gt's K
+    auto qk = [&](int x, uint32_t gt) {  // S_x from CTA tile gt's K (unit 2 gt)
       const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
-      const uint64_t dk = dk0 + (gt & 1) * kStageStep;
+      const uint64_t dk = dk0 + slot_step(2 * gt);
       if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
@@ -894,6 +890,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto commit = [&](int i) {
       if (issuer) umma_commit(bar(i));
     };
+    auto wait_unit = [&](uint32_t u) {
+      return mbar_wait_uniform(bar(kPBarFull + static_cast<int>(u % kSlots)), (u / kSlots) & 1,
+                               abort);
+    };
+    auto free_unit = [&](uint32_t u) { commit(kPBarEmpty + static_cast<int>(u % kSlots)); };
     // Per query tile (scalars): P V products issued and items that used
     // the tile, over all items.
     int pv_count0 = 0, pv_count1 = 0, uses0 = 0, uses1 = 0;
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_uniform(bar(kPBarPFull + x), pv_count & 1, abort)) return false;
       ++pv_count;
       tc_fence_after_sync();
-      const uint64_t dv = dv0 + (gt & 1) * kStageStep;
+      const uint64_t dv = dv0 + slot_step(2 * gt + 1);
       if (issuer) {
 #pragma unroll
         for (int ks = 0; ks < kN / 16; ++ks)
@@ -930,26 +931,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = ig.n0, n1 = ig.n1, n_tiles = ig.n_tiles;
       const uint32_t g0 = g;
       ok = mbar_wait_uniform(bar(a.q_mode ? kPBarQReady : kPBarQFull), k & 1, abort) &&
-           mbar_wait_uniform(bar(kPBarFull + (g0 & 1)), (g0 >> 1) & 1, abort);
+           wait_unit(2 * g0);
       if (!ok) break;
       tc_fence_after_sync();
       qk(0, g0);
       if (n1 > 0) qk(1, g0);
+      free_unit(2 * g0);
       if (n_tiles == 1) commit(kPBarQEmpty);
       for (int j = 0; j < n_tiles && ok; ++j) {
         const uint32_t gj = g0 + static_cast<uint32_t>(j);
         const bool next = j + 1 < n_tiles;
+        if (!(ok = wait_unit(2 * gj + 1))) break;
         if (j < n0) ok = pv(kTile0, j, gj);
         // O_0 is final once its last product is done (not held for tile 1's)
         if (ok && j == n0 - 1) commit(kPBarOFull + 0);
-        if (ok && next) ok = mbar_wait_uniform(bar(kPBarFull + ((gj + 1) & 1)), ((gj + 1) >> 1) & 1, abort);
+        if (ok && next) ok = wait_unit(2 * (gj + 1));
         if (!ok) break;
         tc_fence_after_sync();
         if (next && j + 1 < n0) qk(0, gj + 1);
         if (j < n1 && !(ok = pv(kTile1, j, gj))) break;
         if (j == n1 - 1) commit(kPBarOFull + 1);
-        commit(kPBarEmpty + static_cast<int>(gj & 1));
+        free_unit(2 * gj + 1);
         if (next && j + 1 < n1) qk(1, gj + 1);
+        if (next) free_unit(2 * (gj + 1));
         if (j + 2 == n_tiles) commit(kPBarQEmpty);  // every S of the item issued
       }
       g = g0 + static_cast<uint32_t>(n_tiles);
@@ -1027,26 +1031,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         // crosses some row's last key (warp-uniform) takes the max after
         // the mask instead, so a hidden key never sets the reference.
         float v[kN], mx0, mx1, mx2, mx3;
-        tmem_ld32_max(srow + 0, *reinterpret_cast<float(*)[32]>(&v[0]), mx0);
-        tmem_ld32_max(srow + 32, *reinterpret_cast<float(*)[32]>(&v[32]), mx1);
-        tmem_ld32_max(srow + 64, *reinterpret_cast<float(*)[32]>(&v[64]), mx2);
-        tmem_ld32_max(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
+        if constexpr (kCap) {
+          tmem_ld32_absmax(srow + 0, *reinterpret_cast<float(*)[32]>(&v[0]), mx0);
+          tmem_ld32_absmax(srow + 32, *reinterpret_cast<float(*)[32]>(&v[32]), mx1);
+          tmem_ld32_absmax(srow + 64, *reinterpret_cast<float(*)[32]>(&v[64]), mx2);
+          tmem_ld32_absmax(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
+        } else {
+          tmem_ld32_max(srow + 0, *reinterpret_cast<float(*)[32]>(&v[0]), mx0);
+          tmem_ld32_max(srow + 32, *reinterpret_cast<float(*)[32]>(&v[32]), mx1);
+          tmem_ld32_max(srow + 64, *reinterpret_cast<float(*)[32]>(&v[64]), mx2);
+          tmem_ld32_max(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
+        }
         tmem_ld_wait();
         const int key0 = (kRanges && j >= ig.walk.pre ? j + ig.walk.gap : j) * kN;
-        // Rules: from here v holds scores in log2 units, less row_add.
-        float row_add = 0.f;
-        if constexpr (kCap) cap_scores(v, mx0, mx1, mx2, mx3, a.rules);
-        if constexpr (kBias)
-          row_add = bias_scores<kCap>(v, a.scale_log2, slope, limit - key0,
-                                      key0 + kN - 1 > min_limit);
-        bool masked = key0 + kN - 1 > min_limit;
+        const bool ahead = key0 + kN - 1 > min_limit;  // keys behind some row's query
+        bool masked = ahead;
         if constexpr (kRanges) {
           // some row's window starts inside or behind the tile
           const int window = a.rules.window;
           if (window > 0 && key0 < min_limit + tpt - window) masked = true;
           if (key0 + kN <= d.prefix) masked = false;
         }
-        if (masked || kCap || kBias) {
+        bool near = false;     // rules: scores computed within the exponential's argument
+        float row_add = 0.f;   // rules: what v, or the near form, leaves out of the row's scores
+        float mul = a.scale_log2;
+        if constexpr (kCap || kBias) {
+          const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          bool row_near = true;
+          if constexpr (kCap) row_near = top <= a.rules.near;
+          if constexpr (kBias) row_near = row_near && fabsf(slope) <= kNearBias / 31.f;
+          near = !masked && !(kBias && ahead) && __all_sync(0xffffffffu, row_near);
+          if (near) {
+            const float k = kCap ? a.rules.c1 : a.scale_log2;
+            if constexpr (kBias) {
+              row_add = -slope * static_cast<float>(limit - key0);
+              const float hi = fmaxf(slope * 31.f, 0.f);  // within a load's 32 columns
+              mx0 = fmaf(mx0, k, hi);
+              mx1 = fmaf(mx1, k, hi + slope * 32.f);
+              mx2 = fmaf(mx2, k, hi + slope * 64.f);
+              mx3 = fmaf(mx3, k, hi + slope * 96.f);
+            } else {
+              mx0 *= k;
+              mx1 *= k;
+              mx2 *= k;
+              mx3 *= k;
+            }
+          } else {
+            if constexpr (kCap) cap_scores(v, top, a.rules);
+            if constexpr (kBias)
+              row_add = bias_scores<kCap>(v, a.scale_log2, slope, limit - key0, ahead);
+            mul = 1.f;
+          }
+        }
+        if (masked || ((kCap || kBias) && !near)) {
           if constexpr (kRanges) {
             if (masked) {
               // column cc is seen if lo <= cc <= hi or cc < pre
@@ -1091,28 +1128,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float nm = (m_used == -INFINITY ? 0.f : -m_used) + row_add;
         float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+        // P_x: exp2 of arg(cc), in pairs; keys cc .. cc + 31 -> columns cc / 2 ..
+        auto exponentials = [&](auto arg) {
 #pragma unroll
-        for (int cc = 0; cc < kN; cc += 32) {
-          uint32_t w[16];
+          for (int cc = 0; cc < kN; cc += 32) {
+            uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y0, y1;
-            if constexpr (kCap || kBias) {
-              y0 = v[cc + 2 * e];
-              y1 = v[cc + 2 * e + 1];
-              add2(y0, y1, nm, nm);
-            } else {
-              fma2(y0, y1, v[cc + 2 * e], v[cc + 2 * e + 1], a.scale_log2, nm);
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1;
+              arg(cc + 2 * e, y0, y1);
+              y0 = fast_exp2(y0);
+              y1 = fast_exp2(y1);
+              if (e & 1)
+                add2(sb0, sb1, y0, y1);
+              else
+                add2(sa0, sa1, y0, y1);
+              w[e] = pack_bf16(y0, y1);
             }
-            y0 = fast_exp2(y0);
-            y1 = fast_exp2(y1);
-            if (e & 1)
-              add2(sb0, sb1, y0, y1);
-            else
-              add2(sa0, sa1, y0, y1);
-            w[e] = pack_bf16(y0, y1);
+            tmem_st16u(srow + cc / 2, w);
           }
-          tmem_st16u(srow + cc / 2, w);  // P_x: keys cc .. cc + 31 -> columns cc/2 ..
+        };
+        if constexpr (kCap || kBias) {
+          if (near) {
+            exponentials([&](int cc, float &y0, float &y1) {
+              const float2 s = make_float2(v[cc], v[cc + 1]);
+              float2 t = make_float2(nm, nm);
+              if constexpr (kBias)
+                t = __ffma2_rn(make_float2(slope, slope), make_float2(cc, cc + 1), t);
+              float2 p = make_float2(a.scale_log2, a.scale_log2);
+              if constexpr (kCap) {
+                const float2 u = __fmul2_rn(s, s);
+                p = __ffma2_rn(u, make_float2(a.rules.c5, a.rules.c5),
+                               make_float2(a.rules.c3, a.rules.c3));
+                p = __ffma2_rn(u, p, make_float2(a.rules.c1, a.rules.c1));
+              }
+              p = __ffma2_rn(s, p, t);
+              y0 = p.x;
+              y1 = p.y;
+            });
+          } else {
+            exponentials([&](int cc, float &y0, float &y1) {
+              fma2(y0, y1, v[cc], v[cc + 1], mul, nm);
+            });
+          }
+        } else {
+          exponentials([&](int cc, float &y0, float &y1) {
+            fma2(y0, y1, v[cc], v[cc + 1], a.scale_log2, nm);
+          });
         }
         l = l * f + ((sa0 + sa1) + (sb0 + sb1));
         if (rescale) {

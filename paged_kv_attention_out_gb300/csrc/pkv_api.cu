@@ -278,10 +278,17 @@ static pkv_status score_rules(const pkv_score_mod *mod, float scale, pkv::ScoreR
   if (mod->soft_cap > 0.f) {
     out->cap_in = scale / mod->soft_cap;
     out->cap_log2 = mod->soft_cap * pkv::kLog2e;
-    // the kernels multiply a raw score by cap_in and by twice its log2(e)
-    if (!isfinite(out->cap_in * 4.f) || !isfinite(out->cap_log2) || out->cap_log2 < 1e-30f)
+    // the polynomial's coefficients hold powers of cap_in up to the fourth
+    const double c = static_cast<double>(scale) / mod->soft_cap;
+    if (!(fabs(c) <= 1e6) || !isfinite(out->cap_log2) || out->cap_log2 < 1e-30f)
       return fail(PKV_ERR_INVALID_ARG, "soft_cap %g out of range for scale %g",
                   static_cast<double>(mod->soft_cap), static_cast<double>(scale));
+    const double c1 = static_cast<double>(out->cap_log2) * c;
+    out->c1 = static_cast<float>(c1);
+    out->c3 = static_cast<float>(c1 * c * c * pkv::kTanhNear3);
+    out->c5 = static_cast<float>(c1 * c * c * c * c * pkv::kTanhNear5);
+    out->near = static_cast<float>(
+        fmin(c == 0.0 ? 3e38 : pkv::kTanhNear / fabs(c), c1 == 0.0 ? 3e38 : pkv::kNearLog2 / fabs(c1)));
   }
   out->alibi_slopes = mod->alibi_slopes;
   out->window = mod->window;

@@ -25,6 +25,12 @@ constexpr float kTanh5 = 0.13308174908161163f;
 constexpr float kTanh7 = -0.051947902888059616f;
 constexpr float kTanh9 = 0.015195372514426708f;
 
+// The same on |x| <= kTanhNear with degree five (relative error 4.9e-7): the
+// prefill softmax uses it for tiles whose every score is that near zero.
+constexpr float kTanhNear = 0.25f;
+constexpr double kTanhNear3 = -0.33324571;
+constexpr double kTanhNear5 = 0.12876421;
+
 __device__ __forceinline__ float rule_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -51,11 +57,17 @@ __device__ __forceinline__ float rule_tanh(float x) {
   return fabsf(x) <= kTanhPoly ? near : rule_tanh_far(x);
 }
 
+// `near` also bounds the capped score itself (kNearLog2, log2 units): the
+// prefill softmax takes a bound of a row's scores for their maximum.
+constexpr float kNearLog2 = 16.f;
+
 // The rules of one call, as the kernels take them.
 struct ScoreRules {
   float cap_in;    // scale / cap: x = cap_in * q.k
   float cap_log2;  // cap * log2(e): the capped score in log2 units is cap_log2 tanh x
   const float *alibi_slopes;   // [Hq], or null
+  // cap_log2 tanh(cap_in s) = s (c1 + s^2 (c3 + s^2 c5)) for |s| <= near
+  float near, c1, c3, c5;
   int32_t window;              // > 0: keys at a distance below it; 0: no window
   const int32_t *prefix_lens;  // [batch], or null: first keys that every query sees
 };
