@@ -240,10 +240,12 @@ typedef struct {
  * read, nor are their page_table entries (their pages may have been freed).
  * max_keys_hint: a bound on the keys a request sees, min(seq_len, window +
  * prefix) with a window; it sets the split plan as max_seq_len_hint does, and
- * the workspace is pkv_decode_workspace_size(batch, Hq, Hkv, D,
+ * the workspace is pkv_decode_mod_workspace_size(batch, Hq, Hkv, D,
  * max_keys_hint) bytes. A key on a bad page reads as zeros
  * (PKV_DEVERR_PAGE_RANGE).
  */
+size_t pkv_decode_mod_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t max_keys_hint);
 pkv_status pkv_paged_decode_attn_mod(const pkv_pool *pool, int32_t layer, const void *q, void *o,
                                      float *lse, const int32_t *page_table, int64_t table_stride,
                                      const int32_t *table_idx, const int32_t *seq_lens,

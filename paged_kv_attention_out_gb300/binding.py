@@ -84,6 +84,8 @@ def load() -> ctypes.CDLL:
                                                 _p, _c_int32, _c_int32, ctypes.c_float,
                                                 _c_int32, _p]
     mod_p = ctypes.POINTER(PkvScoreMod)
+    L.pkv_decode_mod_workspace_size.restype = ctypes.c_size_t
+    L.pkv_decode_mod_workspace_size.argtypes = [_c_int32] * 5
     L.pkv_paged_decode_attn_mod.restype = ctypes.c_int
     L.pkv_paged_decode_attn_mod.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _c_int64, _p, _p,
                                             _c_int32, _c_int32, ctypes.c_float, mod_p, _c_int32,
@@ -347,6 +349,12 @@ def pkv_paged_decode_attn(pool, layer: int, q, o, lse, page_table, seq_lens, sca
         ctypes.byref(ps), int(layer), _ptr(q), _ptr(o), _ptr(lse), _ptr(page_table),
         page_table.shape[1], _ptr(table_idx), _ptr(seq_lens), B, Hq, float(scale),
         int(max_seq_len_hint), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def pkv_decode_mod_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                  max_keys_hint: int) -> int:
+    return int(load().pkv_decode_mod_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                    max_keys_hint))
 
 
 def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,

@@ -260,6 +260,21 @@ DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d
   return plan_splits(batch, hq, hkv, d, max_seq_len, sm_count, PKV_CASCADE_UNITS_PER_SM);
 }
 
+// Calls with score rules: half as long splits as plain decode. Rows are ragged
+// (a hint bounds the longest), so the CTAs of the average batch are half the
+// planned ones, and with eight planned per SM the last wave of three resident
+// ones is mostly empty: 8 rows up to 32768 keys of 16 kv heads 183 us at 8, 164
+// at 16, 174 at 32; 64 rows up to 16384 of 8 kv heads 323, 286, 270; with a
+// window of 4096 155, 155, 164.
+#ifndef PKV_RULES_UNITS_PER_SM
+#define PKV_RULES_UNITS_PER_SM 16
+#endif
+
+DecodePlan plan_decode_rules(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
+                             int32_t sm_count) {
+  return plan_splits(batch, hq, hkv, d, max_keys, sm_count, PKV_RULES_UNITS_PER_SM);
+}
+
 static DecodePlan plan_splits(int32_t batch, int32_t hq, int32_t hkv, int32_t d,
                               int32_t max_seq_len, int32_t sm_count, int32_t units_per_sm) {
   (void)hq;

@@ -246,8 +246,9 @@ pkv_status pkv_norm_rope_kv_store(const pkv_pool *pool, int32_t layer, const voi
   a.rot_dim = rot_dim;
   a.positions = positions;
   a.out_loc = out_loc;
+  a.n = num_tokens;
   a.err = d->err;
-  cudaError_t e = pkv::launch_norm_rope_store(g, a, num_tokens, interleaved != 0, stream);
+  cudaError_t e = pkv::launch_norm_rope_store(g, a, interleaved != 0, d->sm_count, stream);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm_rope_kv_store launch");
 }
 
@@ -261,6 +262,22 @@ size_t pkv_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
   return pkv::plan_decode(batch, num_q_heads, num_kv_heads, head_dim,
                           effective_hint(max_seq_len_hint), d->sm_count)
       .workspace_bytes;
+}
+
+size_t pkv_decode_mod_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t max_keys_hint) {
+  // (a call whose rules change nothing runs as plain decode, with its plan)
+  const size_t plain =
+      pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_keys_hint);
+  if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      num_q_heads % num_kv_heads != 0)
+    return 0;
+  DevInfo *d = nullptr;
+  if (device_info(&d) != PKV_OK) return 0;
+  const size_t ruled = pkv::plan_decode_rules(batch, num_q_heads, num_kv_heads, head_dim,
+                                              effective_hint(max_keys_hint), d->sm_count)
+                           .workspace_bytes;
+  return ruled > plain ? ruled : plain;
 }
 
 // The score rules of a call as the kernels take them; *used = false if they
@@ -335,8 +352,11 @@ static pkv_status decode_call(const pkv_pool *pool, int32_t layer, const void *q
     return fail(PKV_ERR_INVALID_ARG, "int32/fp32 tables must be 4-byte aligned");
   DevInfo *d = nullptr;
   if ((s = device_info(&d)) != PKV_OK) return s;
-  const pkv::DecodePlan plan = pkv::plan_decode(batch, num_q_heads, g.hkv, g.d,
-                                                effective_hint(max_seq_len_hint), d->sm_count);
+  const pkv::DecodePlan plan =
+      ruled ? pkv::plan_decode_rules(batch, num_q_heads, g.hkv, g.d,
+                                     effective_hint(max_seq_len_hint), d->sm_count)
+            : pkv::plan_decode(batch, num_q_heads, g.hkv, g.d, effective_hint(max_seq_len_hint),
+                               d->sm_count);
   if (plan.workspace_bytes > 0) {
     if (!workspace)
       return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace is NULL, %zu bytes needed",

@@ -35,6 +35,9 @@ struct DecodePlan {
 
 DecodePlan plan_decode(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_seq_len,
                        int32_t sm_count);
+// The split plan of a decode with score rules.
+DecodePlan plan_decode_rules(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
+                             int32_t sm_count);
 // The split plan of a cascade's suffix decode (host scalars only).
 DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d,
                                int32_t max_seq_len, int32_t sm_count);
@@ -43,7 +46,7 @@ cudaError_t launch_kv_store(const PoolGeom &g, int32_t layer, const void *k, con
                             int64_t row_stride, const int32_t *out_loc, int64_t n,
                             int32_t sm_count, unsigned *err, cudaStream_t stream);
 
-// Norm + rotation of q and k, append of k and v (norm_rope.cu). n < 2^31 tokens.
+// Norm + rotation of q and k, append of k and v (norm_rope.cu). 0 < n < 2^31 tokens.
 struct NormRopeArgs {
   __nv_bfloat16 *pool;
   int64_t plane;
@@ -66,10 +69,11 @@ struct NormRopeArgs {
   int32_t rot_dim;  // 0: no rotation, else a multiple of 16
   const int32_t *positions;
   const int32_t *out_loc;
+  int64_t n;
   unsigned *err;
 };
-cudaError_t launch_norm_rope_store(const PoolGeom &g, const NormRopeArgs &a, int64_t n,
-                                   bool interleaved, cudaStream_t stream);
+cudaError_t launch_norm_rope_store(const PoolGeom &g, const NormRopeArgs &a, bool interleaved,
+                                   int32_t sm_count, cudaStream_t stream);
 
 cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void *o, float *lse,
                           const int32_t *page_table, int64_t table_stride,

@@ -77,7 +77,7 @@ def mod_run(rules, inputs=None, hint=None, scale=None, lse=True, before=None):
     scale = case.scale if scale is None else scale
     if case.kind == "decode":
         h = rules.max_keys() if hint is None else hint
-        n = pkv.pkv_decode_workspace_size(case.B, case.Hq, case.Hkv, case.D, h)
+        n = pkv.pkv_decode_mod_workspace_size(case.B, case.Hq, case.Hkv, case.D, h)
         ws = torch.full((max(n, 1),), 0xff, dtype=torch.uint8, device="cuda")
         pkv.pkv_paged_decode_attn_mod(pool, case.layer, q, o, l, t["page_table"], t["seq_lens"],
                                       scale, h, ws, table_idx=t.get("table_idx"), **rules.kwargs())
@@ -309,3 +309,19 @@ def test_refusals(call, mod):
     pool = binding.PkvPool(1 << 30, 1, 10, 16, 2, 64)
     assert call(binding.load(), pool, binding.PkvScoreMod(*mod)) == 1
     assert b"pool" not in binding.load().pkv_last_error()
+
+
+@pytest.mark.gpu
+def test_the_workspace_covers_both_plans_and_a_smaller_one_is_refused():
+    import paged_kv_attention_out_gb300 as pkv
+    case = W.random_case(15, seq_lens=[5000, 300], Hq=8, Hkv=2, D=64, P=16)
+    pool, k, v, q, t = gpu_inputs(case)
+    o, lse = nan_outputs(q)
+    n = pkv.pkv_decode_mod_workspace_size(2, 8, 2, 64, 5000)
+    assert n >= pkv.pkv_decode_workspace_size(2, 8, 2, 64, 5000) > 0
+    ws = torch.empty(n - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.pkv_paged_decode_attn_mod(pool, 0, q, o, lse, t["page_table"], t["seq_lens"],
+                                      case.scale, 5000, ws, soft_cap=5.0)
+    assert e.value.status == 3
+    assert pkv.pkv_decode_mod_workspace_size(0, 8, 2, 64, 5000) == 0
