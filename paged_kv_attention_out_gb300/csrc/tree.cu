@@ -63,7 +63,8 @@ constexpr uint32_t kTmemO = 256;  // O_x at 256 + 128 x
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxTree = PKV_MAX_TREE_TOKENS;
 constexpr int kMaskWords = kMaxTree / 32;
-constexpr int kMinTiles = 2;  // smallest share of a group: two key tiles
+constexpr int kMinTiles = 4;    // smallest share of a group, in key tiles
+constexpr int kBlockTiles = 2;  // cost of a block's prologue and epilogue, in key tiles
 // Cost of a key tile for a block of one and of two query tiles. At D = 128
 // both are near the tile's 64 KB at the copy rate (64 drafts: 171, 170, 169 and
 // 176 us for 1:1, 5:6, 3:4 and 3:5; 33 drafts: 153, 155, 155 and 163); at 64
@@ -155,7 +156,8 @@ struct TreeArgs {
 // One query block: up to kQT tokens_per_tile tokens of one request.
 struct Block {
   int req, sub, t_base, tokens, p, c, seq, tiles;
-  int cost;  // of a key tile
+  int cost;   // of a key tile
+  int extra;  // of the block's prologue and epilogue, added to its first tile's
 };
 
 // Block b of the call, tiles = 0 if there is nothing to compute. Keys behind
@@ -184,15 +186,27 @@ __device__ __forceinline__ Block load_block(const TreeArgs &a, int b, bool repor
   k.t_base = beg + k.sub * tpb;
   k.tokens = min(tpb, k.c - k.sub * tpb);
   k.cost = k.tokens <= a.tokens_per_tile ? a.cost.one : a.cost.two;
+  k.extra = kBlockTiles * a.cost.one;
   k.tiles = k.tokens > 0 ? (k.p + k.sub * tpb + k.tokens + kN - 1) / kN : 0;
   return k;
+}
+
+// Quotients of non-negative numbers, in 32 bits where they fit (a 64-bit
+// division takes a tenth of a microsecond, and several lie on the way to the
+// first load).
+__device__ __forceinline__ long long div_down(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+__device__ __forceinline__ long long div_up(long long x, long long y) {
+  return div_down(x + y - 1, y);
 }
 
 // A CTA's walk over its share of the tiles; every role keeps its own copy.
 struct Walk {
   int block;      // of the next segment
   int skip;       // tiles of it that belong to an earlier group
-  int64_t left;   // cost of the share from the next tile on
+  long long left;  // cost of the share from the next tile on
 };
 
 struct Segment {
@@ -211,12 +225,13 @@ __device__ __forceinline__ bool next_segment(const TreeArgs &a, Walk &w, Segment
     s.tile0 = w.skip;
     w.skip = 0;
     if (s.tile0 >= s.b.tiles) continue;
-    // the tiles that begin within the share
-    s.n = static_cast<int>(min(static_cast<int64_t>(s.b.tiles - s.tile0),
-                               (w.left + s.b.cost - 1) / s.b.cost));
+    // the tiles that begin within the share (the second begins extra later)
+    const long long extra = s.tile0 == 0 ? s.b.extra : 0;
+    const long long n = w.left > extra ? div_up(w.left - extra, s.b.cost) : 0;
+    s.n = static_cast<int>(min(static_cast<long long>(s.b.tiles - s.tile0), n > 1 ? n : 1ll));
     s.whole = s.n == s.b.tiles;
     s.slot = 2 * static_cast<int>(blockIdx.y) + (s.tile0 == 0 ? 1 : 0);
-    w.left -= static_cast<int64_t>(s.n) * s.b.cost;
+    w.left -= extra + static_cast<long long>(s.n) * s.b.cost;
     return true;
   }
   return false;
@@ -336,14 +351,18 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       return v + before;
     };
     long long total = 0, round;
-    auto cost_of = [&](int b, bool report, int &cost) -> long long {
-      cost = 1;
+    struct Cost {
+      int tiles, unit, extra;
+    };
+    auto cost_of = [&](int b, bool report, Cost &c) -> long long {
+      c = Cost{0, 1, 0};
       if (b >= nblocks) return 0;
       const Block k = load_block<kQT>(a, b, report);
-      cost = max(k.cost, 1);
-      return static_cast<long long>(k.tiles) * k.cost;
+      if (k.tiles == 0) return 0;
+      c = Cost{k.tiles, k.cost, k.extra};
+      return k.extra + static_cast<long long>(k.tiles) * k.cost;
     };
-    int unit0, unit;
+    Cost unit0, unit;
     const long long mine = cost_of(tid, lead, unit0);
     const long long first_end = scan(mine, round);
     const long long first_total = round;
@@ -353,8 +372,8 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       total += round;
     }
     // at least one tile begins in every share that a block covers
-    const long long per = max(static_cast<long long>(max(kMinTiles * a.cost.one, a.cost.two)),
-                              (total + a.groups - 1) / a.groups);
+    const int least = max(kMinTiles * a.cost.one, kBlockTiles * a.cost.one + a.cost.two);
+    const long long per = max(static_cast<long long>(least), div_up(total, a.groups));
     const long long lo = per * blockIdx.y;
     const long long hi = min(total, lo + per);
     long long base = 0;
@@ -369,14 +388,19 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       end += base;
       const long long start = end - cost;
       if (cost > 0 && start <= lo && lo < end && lo < hi) {
-        const long long skip = (lo - start + unit - 1) / unit;
-        s_walk = Walk{b, static_cast<int>(skip), hi - (start + skip * unit)};
+        // the first tile that begins in the share
+        const long long first =
+            lo > start ? max(1ll, div_up(max(0ll, lo - start - unit.extra), unit.unit)) : 0;
+        const long long at = start + (first > 0 ? unit.extra : 0) + first * unit.unit;
+        s_walk = Walk{b, static_cast<int>(first), hi - at};
       }
       if (lead && b < nblocks && a.groups > 1) {
         // which groups the block's tiles begin in (the merge reads this)
         int2 e = make_int2(-1, -1);
         if (cost > 0) {
-          const int g0 = static_cast<int>(start / per), g1 = static_cast<int>((end - unit) / per);
+          const long long last = unit.tiles > 1 ? end - unit.unit : start;
+          const int g0 = static_cast<int>(div_down(start, per));
+          const int g1 = static_cast<int>(div_down(last, per));
           if (g1 > g0) e = make_int2(g0, g1);
         }
         a.table[b] = e;
@@ -984,14 +1008,14 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
 // lse) o_s. One CTA per (block, kv head, 32 rows), eight warps with D / 8
 // columns each; lane = row, so the states' [column group][row] layout is read
 // in whole lines. States are taken kBatch at a time, all their loads together,
-// with a running maximum: one round trip to L2 for the usual two or three.
+// with a running maximum: one round trip to L2 for the usual two.
 constexpr int kMergeThreads = 256;
 
 template <int D, int kQT>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a) {
   constexpr int kRows = kQT * kM;
   constexpr int kCols = D / 4 / (kMergeThreads / 32);  // float4 columns per warp
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 2;
   const int b = blockIdx.x;
   // inputs of the call, complete before any CTA of tree_kernel went on
   const Block k = load_block<kQT>(a, b, false);
