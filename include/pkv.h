@@ -139,7 +139,7 @@ pkv_status pkv_kv_store(const pkv_pool *pool, int32_t layer, const void *k, cons
  * outside the table is skipped (PKV_DEVERR_POSITION: its q_out row is not
  * written either); one whose slot is outside the pool is not stored, only its
  * q_out row is written (PKV_DEVERR_OUT_LOC_RANGE). Two tokens with the same
- * slot give an unspecified one of the two rows. v's bits are copied unchanged.
+ * slot leave that slot's row unspecified. v's bits are copied unchanged.
  */
 pkv_status pkv_norm_rope_kv_store(const pkv_pool *pool, int32_t layer, const void *q,
                                   int64_t q_row_stride, void *q_out, int32_t num_q_heads,
@@ -373,9 +373,16 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
  * with chunk query j of request r at position t = p_r + j; mod NULL: none. A
  * prefix that reaches past the chunk ends with the request's keys (seq_lens[r]).
  * Keys that no query of the request's chunk sees are not read, nor are their
- * page_table entries. Hints, workspace and refusals as for
- * pkv_paged_extend_attn (the workspace still has room for every key).
+ * page_table entries. Hints and refusals as for pkv_paged_extend_attn; the
+ * workspace is pkv_extend_mod_workspace_size(batch, total_q, Hq, Hkv, D,
+ * max_seq_len_hint, max_total_keys_hint) bytes. A call with few queries (up to
+ * 256 requests and 352 query blocks of 256 / (Hq / Hkv) tokens) reads K/V
+ * straight from the pool; there a request past max_total_keys_hint is computed
+ * all the same.
  */
+size_t pkv_extend_mod_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t max_seq_len_hint, int64_t max_total_keys_hint);
 pkv_status pkv_paged_extend_attn_mod(const pkv_pool *pool, int32_t layer, const void *q,
                                      const int32_t *qo_indptr, void *o, float *lse,
                                      const int32_t *page_table, int64_t table_stride,

@@ -11,6 +11,7 @@ from .binding import (PkvError, pkv_cascade_workspace_size,  # noqa: F401
                       pkv_paged_decode_attn_noalloc, pkv_paged_decode_attn_store,
                       pkv_paged_extend_attn, pkv_paged_extend_attn_store,
                       pkv_paged_tree_attn, pkv_tree_workspace_size,
-                      pkv_decode_mod_workspace_size, pkv_paged_decode_attn_mod,
+                      pkv_decode_mod_workspace_size, pkv_extend_mod_workspace_size,
+                      pkv_paged_decode_attn_mod,
                       pkv_paged_extend_attn_mod,
                       pkv_read_device_errors)

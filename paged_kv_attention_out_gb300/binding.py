@@ -90,6 +90,8 @@ def load() -> ctypes.CDLL:
     L.pkv_paged_decode_attn_mod.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _c_int64, _p, _p,
                                             _c_int32, _c_int32, ctypes.c_float, mod_p, _c_int32,
                                             _p, ctypes.c_size_t, _p]
+    L.pkv_extend_mod_workspace_size.restype = ctypes.c_size_t
+    L.pkv_extend_mod_workspace_size.argtypes = [_c_int32] * 6 + [_c_int64]
     L.pkv_paged_extend_attn_mod.restype = ctypes.c_int
     L.pkv_paged_extend_attn_mod.argtypes = [pool_p, _c_int32, _p, _p, _p, _p, _p, _c_int64, _p,
                                             _p, _c_int32, _c_int32, _c_int32, ctypes.c_float,
@@ -314,7 +316,7 @@ def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc,
         if k_norm.shape[0] != d:
             raise ValueError("k_norm must have head_dim entries")
     _check(load().pkv_norm_rope_kv_store(
-        ctypes.byref(ps), layer, qp, qs, op, hq, kp, vp, ks, qn, kn, eps, tp, rows, rot,
+        ctypes.byref(ps), int(layer), qp, qs, op, hq, kp, vp, ks, qn, kn, float(eps), tp, rows, rot,
         bool(interleaved), pp, _ints(out_loc, n, dev, "out_loc"), n, _stream(stream)))
 
 
@@ -366,7 +368,7 @@ def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,
             raise ValueError("alibi_slopes must have one entry per q head")
     if prefix_lens is not None:
         pp = _ints(prefix_lens, batch, dev, "prefix_lens")
-    return PkvScoreMod(soft_cap, sp, window, pp)
+    return PkvScoreMod(float(soft_cap), sp, int(window), pp)
 
 
 def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens, scale: float,
@@ -386,8 +388,8 @@ def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens,
     mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_decode_attn_mod(
-        ctypes.byref(ps), layer, qp, op, lp, pp, stride, tp, sp, B, Hq, scale, ctypes.byref(mod),
-        max_keys_hint, ws, ws_bytes, _stream(stream)))
+        ctypes.byref(ps), int(layer), qp, op, lp, pp, stride, tp, sp, B, Hq, float(scale), ctypes.byref(mod),
+        int(max_keys_hint), ws, ws_bytes, _stream(stream)))
 
 
 def pkv_paged_decode_attn_store(pool, layer: int, q, k_new, v_new, o, lse, page_table, seq_lens,
@@ -495,6 +497,14 @@ def pkv_paged_extend_attn(pool, layer: int, q, qo_indptr, o, lse, page_table, se
         _stream(stream)))
 
 
+def pkv_extend_mod_workspace_size(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int,
+                                  head_dim: int, max_seq_len_hint: int,
+                                  max_total_keys_hint: int = 0) -> int:
+    return int(load().pkv_extend_mod_workspace_size(batch, total_q, num_q_heads, num_kv_heads,
+                                                    head_dim, max_seq_len_hint,
+                                                    int(max_total_keys_hint)))
+
+
 def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table, seq_lens,
                               scale: float, max_seq_len_hint: int, workspace,
                               soft_cap: float = 0.0, alibi_slopes=None, window: int = 0,
@@ -514,8 +524,8 @@ def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table
     mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_extend_attn_mod(
-        ctypes.byref(ps), layer, qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"), op, lp, pp, stride,
-        tp, sp, B, T, Hq, scale, ctypes.byref(mod), max_seq_len_hint, max_total_keys_hint, ws,
+        ctypes.byref(ps), int(layer), qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"), op, lp, pp, stride,
+        tp, sp, B, T, Hq, float(scale), ctypes.byref(mod), int(max_seq_len_hint), int(max_total_keys_hint), ws,
         ws_bytes, _stream(stream)))
 
 
@@ -583,9 +593,9 @@ def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_ta
     pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_tree_attn(
-        ctypes.byref(ps), layer, qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"),
-        _ints(parents, T, dev, "parents"), op, lp, pp, stride, tp, sp, B, T, Hq, scale,
-        max_tree_tokens, max_seq_len_hint, ws, ws_bytes, _stream(stream)))
+        ctypes.byref(ps), int(layer), qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"),
+        _ints(parents, T, dev, "parents"), op, lp, pp, stride, tp, sp, B, T, Hq, float(scale),
+        int(max_tree_tokens), int(max_seq_len_hint), ws, ws_bytes, _stream(stream)))
 
 
 def pkv_cascade_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpkv.so")
 SOURCES = ["pkv_api.cu", "kv_store.cu", "norm_rope.cu", "decode.cu", "extend.cu", "cascade.cu",
-           "tree.cu", "merge.cu", "decode_noalloc.cu", "tensor_map.cu"]
+           "tree.cu", "extend_direct.cu", "extend_direct_64.cu", "extend_direct_128.cu",
+           "merge.cu", "decode_noalloc.cu", "tensor_map.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

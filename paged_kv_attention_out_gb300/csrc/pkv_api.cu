@@ -531,6 +531,35 @@ size_t pkv_extend_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t he
       .total_bytes;
 }
 
+size_t pkv_extend_mod_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t max_seq_len_hint, int64_t max_total_keys_hint) {
+  const size_t gathered = pkv_extend_workspace_size(batch, num_kv_heads, head_dim,
+                                                    max_seq_len_hint, max_total_keys_hint);
+  if (gathered == 0 || total_q <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 16)
+    return 0;
+  DevInfo *d = nullptr;
+  if (device_info(&d) != PKV_OK) return 0;
+  pkv::DirectPlan plan;
+  if (!pkv::extend_direct_plan(batch, total_q, num_q_heads, num_kv_heads, head_dim,
+                               max_seq_len_hint, d->sm_count, &plan))
+    return gathered;
+  return plan.workspace_bytes > gathered ? plan.workspace_bytes : gathered;
+}
+
+static pkv_status check_workspace(const void *workspace, size_t workspace_bytes, size_t need) {
+  if (need == 0) return PKV_OK;
+  if (!workspace)
+    return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace is NULL, %zu bytes needed", need);
+  if (workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", workspace_bytes,
+                need);
+  if (!aligned(workspace, 256))
+    return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return PKV_OK;
+}
+
 // Extend with (k_new != NULL) or without the fused store of the chunk's K/V.
 static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q,
                               const void *k_new, const void *v_new, int64_t kv_row_stride,
@@ -574,6 +603,21 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
   if (cap > (int64_t(1) << 30)) return fail(PKV_ERR_UNSUPPORTED, "sequence capacity too large");
   if (max_total_keys_hint > (int64_t(1) << 40))
     return fail(PKV_ERR_UNSUPPORTED, "max_total_keys_hint too large");
+  if (ruled) {
+    // few query blocks: straight from the pool, the work shared out by key tiles
+    DevInfo *d = nullptr;
+    if ((s = device_info(&d)) != PKV_OK) return s;
+    pkv::DirectPlan plan;
+    if (pkv::extend_direct_plan(batch, total_q, num_q_heads, g.hkv, g.d,
+                                static_cast<int32_t>(cap), d->sm_count, &plan)) {
+      if ((s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)
+        return s;
+      const cudaError_t e = pkv::launch_extend_direct(
+          g, layer, q, qo_indptr, o, lse, page_table, table_stride, table_idx, seq_lens, batch,
+          total_q, num_q_heads, scale, rules, plan, workspace, d->err, stream);
+      return e == cudaSuccess ? PKV_OK : cuda_fail(e, "extend launch");
+    }
+  }
   const pkv::ExtendLayout lay = pkv::extend_layout(batch, g.hkv, g.d, cap, max_total_keys_hint);
   if (2 * g.hkv * lay.cap_rows >= (int64_t(1) << 31) || lay.max_blocks >= (int64_t(1) << 28))
     return fail(PKV_ERR_UNSUPPORTED, "extend: kv heads x key bound too large (%lld rows)",
@@ -711,19 +755,10 @@ pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *
   if (cap > row_capacity) cap = row_capacity;
   DevInfo *d = nullptr;
   if ((s = device_info(&d)) != PKV_OK) return s;
-  const pkv::TreePlan plan =
+  const pkv::DirectPlan plan =
       pkv::tree_plan(batch, num_q_heads, g.hkv, g.d, max_tree_tokens, static_cast<int32_t>(cap),
                      d->sm_count);
-  if (plan.workspace_bytes > 0) {
-    if (!workspace)
-      return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace is NULL, %zu bytes needed",
-                  plan.workspace_bytes);
-    if (workspace_bytes < plan.workspace_bytes)
-      return fail(PKV_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", workspace_bytes,
-                  plan.workspace_bytes);
-    if (!aligned(workspace, 256))
-      return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  }
+  if ((s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK) return s;
   cudaError_t e = pkv::launch_tree(g, layer, q, qo_indptr, parents, o, lse, page_table,
                                    table_stride, table_idx, seq_lens, batch, total_q, num_q_heads,
                                    scale, max_tree_tokens, plan, workspace, d->err, stream);

@@ -151,25 +151,39 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
                           void *workspace, int32_t sm_count, unsigned *err, cudaStream_t stream,
                           const ExtendMode &mode = ExtendMode());
 
-// Draft-tree attention (tree.cu): query tiles per block, query blocks per
-// request, groups the work is cut for, and the workspace (0 bytes for one
-// group), all from host scalars.
-struct TreePlan {
+// Attention straight from the pool (direct_tc.cuh): query tiles per block, a
+// bound on the query blocks, groups the work is cut for, and the workspace (0
+// bytes for one group), all from host scalars.
+struct DirectPlan {
   int32_t query_tiles;
-  int32_t blocks_per_req;
+  int32_t max_blocks;
   int32_t groups;
   size_t lse_offset;
   size_t table_offset;
   size_t workspace_bytes;
 };
-TreePlan tree_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_tree,
-                   int32_t max_seq, int32_t sm_count);
+
+// Draft-tree attention (tree.cu).
+DirectPlan tree_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_tree,
+                     int32_t max_seq, int32_t sm_count);
 cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const int32_t *qo_indptr,
                         const int32_t *parents, void *o, float *lse, const int32_t *page_table,
                         int64_t table_stride, const int32_t *table_idx, const int32_t *seq_lens,
                         int32_t batch, int32_t total_q, int32_t hq, float scale, int32_t max_tree,
-                        const TreePlan &plan, void *workspace, unsigned *err,
+                        const DirectPlan &plan, void *workspace, unsigned *err,
                         cudaStream_t stream);
+
+// Extend under score rules with few query blocks (extend_direct.cu); false:
+// more blocks or requests than it takes.
+bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
+                        int32_t max_seq, int32_t sm_count, DirectPlan *plan);
+cudaError_t launch_extend_direct(const PoolGeom &g, int32_t layer, const void *q,
+                                 const int32_t *qo_indptr, void *o, float *lse,
+                                 const int32_t *page_table, int64_t table_stride,
+                                 const int32_t *table_idx, const int32_t *seq_lens, int32_t batch,
+                                 int32_t total_q, int32_t hq, float scale, const ScoreRules &rules,
+                                 const DirectPlan &plan, void *workspace, unsigned *err,
+                                 cudaStream_t stream);
 
 cudaError_t launch_merge(const float *o_a, const float *lse_a, const float *o_b,
                          const float *lse_b, void *o_out, bool out_bf16, float *lse_out,

@@ -72,4 +72,93 @@ struct ScoreRules {
   const int32_t *prefix_lens;  // [batch], or null: first keys that every query sees
 };
 
+// The key tiles of a block of queries whose first one is at position t0, in
+// the order walked: tiles 0 .. pre - 1 hold the always visible prefix, tile v
+// >= pre of the walk is tile v + gap of the request.
+constexpr int kRuleTile = 128;  // keys
+struct TileWalk {
+  int pre, gap;
+};
+__device__ __forceinline__ TileWalk tile_walk(int t0, int window, int prefix) {
+  const int first = window > 0 ? max(0, t0 - window + 1) / kRuleTile : 0;
+  TileWalk w;
+  w.pre = min((prefix + kRuleTile - 1) / kRuleTile, first);
+  w.gap = first - w.pre;
+  return w;
+}
+
+// The request's always visible keys, within its row.
+__device__ __forceinline__ int rule_prefix(const int32_t *prefix_lens, int r, int seq) {
+  return prefix_lens ? min(max(prefix_lens[r], 0), seq) : 0;
+}
+
+// The prefill softmax's part of the rules (a row of kRuleTile scores a thread).
+// A tile is near if a bound of each row's scores comes with the loads (the
+// largest absolute raw score of each 32 columns under a cap, the largest raw
+// one under a bias alone), every raw score is in the short polynomial's range,
+// no column is masked and the bias is not so steep that the bound would be far
+// off. Its scores are then computed within the exponential's argument, in pairs
+// on the FMA pipe:
+//   y = s (c1 + u (c3 + u c5)) [+ slope cc] + (row terms - m),   u = s^2
+// three packed instructions more per pair for a cap, one for a bias, and the
+// reference m is that bound (at most 2 kNearLog2 + kNearBias above the row's
+// maximum, so nothing that counts underflows). Other tiles take the general
+// way: every score in place, masked, then its true maximum.
+constexpr float kNearBias = 46.f;  // most a bias may change within 32 columns, log2 units
+
+template <bool kCap, bool kBias>
+__device__ __forceinline__ void near_pair(float s0, float s1, int cc, float scale_log2,
+                                          float slope, float row, const ScoreRules &rules,
+                                          float &y0, float &y1) {
+  const float2 s = make_float2(s0, s1);
+  float2 t = make_float2(row, row);
+  if constexpr (kBias) t = __ffma2_rn(make_float2(slope, slope), make_float2(cc, cc + 1), t);
+  float2 p = make_float2(scale_log2, scale_log2);
+  if constexpr (kCap) {
+    const float2 u = __fmul2_rn(s, s);
+    p = __ffma2_rn(u, make_float2(rules.c5, rules.c5), make_float2(rules.c3, rules.c3));
+    p = __ffma2_rn(u, p, make_float2(rules.c1, rules.c1));
+  }
+  p = __ffma2_rn(s, p, t);
+  y0 = p.x;
+  y1 = p.y;
+}
+
+// All scores of a tile in log2 units, in place, without the bias; top: the
+// largest absolute raw score of the thread's row.
+__device__ __forceinline__ void cap_scores(float (&v)[kRuleTile], float top,
+                                           const ScoreRules &rules) {
+  if (__all_sync(0xffffffffu, top <= rules.near)) {
+#pragma unroll
+    for (int cc = 0; cc < kRuleTile; ++cc) {
+      const float u = v[cc] * v[cc];
+      v[cc] *= fmaf(u, fmaf(u, rules.c5, rules.c3), rules.c1);
+    }
+  } else {
+#pragma unroll
+    for (int cc = 0; cc < kRuleTile; ++cc)
+      v[cc] = rules.cap_log2 * rule_tanh_far(v[cc] * rules.cap_in);
+  }
+}
+
+// Scores in log2 units less slope times the distance, for the row whose query
+// is at column t of the tile (t < 0 or past its end for most). A row's
+// -slope t is the same for the whole tile: it is returned, not added, unless
+// the tile holds keys behind some row's query (ahead), whose distance is cc - t.
+template <bool kScaled>
+__device__ __forceinline__ float bias_scores(float (&v)[kRuleTile], float scale_log2, float slope,
+                                             int t, bool ahead) {
+  const float ft = static_cast<float>(t);
+  if (ahead) {
+#pragma unroll
+    for (int cc = 0; cc < kRuleTile; ++cc)
+      v[cc] = fmaf(-slope, fabsf(ft - cc), kScaled ? v[cc] : v[cc] * scale_log2);
+    return 0.f;
+  }
+#pragma unroll
+  for (int cc = 0; cc < kRuleTile; ++cc)
+    v[cc] = fmaf(slope, cc, kScaled ? v[cc] : v[cc] * scale_log2);
+  return -slope * ft;
+}
+
 }  // namespace pkv

@@ -66,7 +66,7 @@ class Rules:
         return attend(kv, q, qo, case.scale if scale is None else scale, self.visible, self.rule)
 
 
-def mod_run(rules, inputs=None, hint=None, scale=None, lse=True, before=None):
+def mod_run(rules, inputs=None, hint=None, scale=None, lse=True, before=None, stale=None):
     import paged_kv_attention_out_gb300 as pkv
     case = rules.case
     pool, k, v, q, t = inputs or gpu_inputs(case)
@@ -83,8 +83,11 @@ def mod_run(rules, inputs=None, hint=None, scale=None, lse=True, before=None):
                                       scale, h, ws, table_idx=t.get("table_idx"), **rules.kwargs())
     else:
         h, total = case.max_seq_len, int(case.seq_lens.sum())
-        n = pkv.pkv_extend_workspace_size(case.B, case.Hkv, case.D, h, total)
+        n = pkv.pkv_extend_mod_workspace_size(case.B, case.total_q, case.Hq, case.Hkv, case.D, h,
+                                              total)
         ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")  # NaN bits
+        if stale is not None:  # what an earlier call may have left
+            ws[:n // 16 * 16].view(torch.int32).view(-1, 4)[:] = torch.tensor(stale).cuda()
         pkv.pkv_paged_extend_attn_mod(pool, case.layer, q, t["qo_indptr"], o, l, t["page_table"],
                                       t["seq_lens"], scale, h, ws, table_idx=t.get("table_idx"),
                                       max_total_keys_hint=total, **rules.kwargs())
@@ -126,6 +129,65 @@ def test_extend_rules(rule, D, P, Hq, Hkv):
     case = W.random_case(4, kind="extend", seq_lens=[1, 160, 513, 260, 700],
                          chunk_lens=[1, 160, 13, 129, 70], Hq=Hq, Hkv=Hkv, D=D, P=P,
                          use_table_idx=True)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", RULES, ids=str)
+@pytest.mark.parametrize("D,P,Hq,Hkv", [(64, 1, 4, 4), (128, 16, 8, 2)])
+def test_extend_rules_of_many_requests(rule, D, P, Hq, Hkv):
+    """More requests than the direct form takes: keys gathered first, blocks in order of cost."""
+    rng = np.random.default_rng(1)
+    chunks = np.concatenate([[129, 70], rng.integers(1, 3, 270)])
+    seqs = np.concatenate([[513, 300], chunks[2:] + rng.integers(0, 40, 270)])
+    case = W.random_case(16, kind="extend", seq_lens=seqs, chunk_lens=chunks, Hq=Hq, Hkv=Hkv, D=D,
+                         P=P)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", [dict(cap=3.0, alibi=True, window=50), dict(prefix=[30])], ids=str)
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+def test_scales_of_many_requests(rule, scale):
+    case = W.random_case(17, kind="extend", seq_lens=[150] + [5] * 260, chunk_lens=[64] + [2] * 260,
+                         Hq=4, Hkv=2, D=64, P=16)
+    mod_check(Rules(case, **rule), scale=scale)
+
+
+@pytest.mark.gpu
+def test_extend_tables_are_checked_in_both_forms():
+    """Malformed qo_indptr, lengths past the row and bad pages are flagged; others are computed."""
+    import paged_kv_attention_out_gb300 as pkv
+    for more in (0, 260):
+        case = W.random_case(18, kind="extend", seq_lens=[100, 300, 64] + [3] * more,
+                             chunk_lens=[40, 100, 20] + [2] * more, Hq=4, Hkv=2, D=64, P=16)
+        rules = Rules(case, window=70, cap=20.0)
+        want = rules.want()
+        qo = case.qo_indptr
+
+        def flagged(bit, ok, change):
+            pkv.pkv_read_device_errors()
+            o, lse = mod_run(rules, before=change)
+            assert pkv.pkv_read_device_errors() == bit
+            check(o, lse, want, np.concatenate([np.arange(qo[r], qo[r + 1]) for r in ok]))
+
+        def set_(name, at, value):
+            def change(pool, t):
+                t[name][at] = value
+            return change
+
+        flagged(0x4, [0], set_("seq_lens", 1, case.page_table.shape[1] * 16 + 1))
+        flagged(0x8, [0], set_("seq_lens", 1, 50))
+        flagged(PAGE, [0, 2], set_("page_table", (1, 18), case.NP + 3))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [1, 16])
+@pytest.mark.parametrize("rule", [dict(cap=30.0), dict(window=1000, prefix=[200]),
+                                  dict(alibi=True)], ids=str)
+def test_a_short_chunk_over_a_long_prefix_is_shared_by_the_whole_gpu(rule, P):
+    case = W.random_case(19, kind="extend", seq_lens=[9000, 130], chunk_lens=[20, 3], Hq=8, Hkv=2,
+                         D=128, P=P)
     mod_check(Rules(case, **rule))
 
 
@@ -221,6 +283,15 @@ def test_empty_rows_and_prefix_clipping():
 
 
 @pytest.mark.gpu
+def test_a_workspace_of_any_contents():
+    """The block table's entries past the call's last block must not be taken for blocks: here
+    they would name token 0 (and its group's states), which a later block would overwrite."""
+    case = W.random_case(20, kind="extend", seq_lens=[900, 300, 700, 5], chunk_lens=[70, 1, 33, 5],
+                         Hq=8, Hkv=2, D=64, P=16)
+    mod_check(Rules(case, cap=20.0), stale=[0, 0, 0, 1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("hint", [0, 16, 5000])
 def test_decode_hint_changes_only_the_splits(hint):
     case = W.random_case(12, seq_lens=[2000, 100], Hq=8, Hkv=2, D=64, P=16)
@@ -238,7 +309,7 @@ def test_a_chunked_prompt_equals_the_whole():
     import paged_kv_attention_out_gb300 as pkv
     pool, k, v, q, t = gpu_inputs(whole)
     pkv.pkv_kv_store(pool, 0, k, v, t["out_loc"])
-    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
     parts = []
     for a, b in ((0, 130), (130, 300)):
         qo = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
@@ -260,7 +331,7 @@ def test_replay_in_a_graph_follows_new_lengths(kind):
     pool, k, v, q, t = gpu_inputs(case)
     pkv.pkv_kv_store(pool, 0, k, v, t["out_loc"])
     o, lse = nan_outputs(q)
-    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
     args = rules.kwargs()
 
     def call():
