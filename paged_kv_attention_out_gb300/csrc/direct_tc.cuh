@@ -246,8 +246,8 @@ __device__ __forceinline__ Block load_block(const DirectArgs &a, const Blocks &b
 
 // First key of the block's tile v.
 template <int kRules>
-__device__ __forceinline__ int tile_key(const Block &k, int v) {
-  return (kRules != 0 && v >= k.walk.pre ? v + k.walk.gap : v) * kN;
+__device__ __forceinline__ int tile_key(const TileWalk &w, int v) {
+  return (kRules != 0 && v >= w.pre ? v + w.gap : v) * kN;
 }
 
 // Quotients of non-negative numbers, in 32 bits where they fit (a 64-bit
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       const int box = kTma ? a.box : 1;
       auto box_key = [&](int j, int g) -> int {
         const int at = kTma ? lane * box : g * 32 + lane;
-        const int key = tile_key<kRules>(sg.b, sg.tile0 + j) + at;
+        const int key = tile_key<kRules>(sg.b.walk, sg.tile0 + j) + at;
         if (kRules != 0 && key >= sg.b.prefix && key + box <= sg.b.lo) return -1;  // seen by none
         return at < kN && key < sg.b.seq ? key : -1;
       };
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       for (uint32_t w = first; w < n_units; w += kProducerWarps) {
         const int j = static_cast<int>(w >> 1), c = static_cast<int>(w & 1);
         const uint32_t u = u0 + w;
-        const int key0 = tile_key<kRules>(sg.b, sg.tile0 + j);
+        const int key0 = tile_key<kRules>(sg.b.walk, sg.tile0 + j);
         long long cur[kGroups];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) cur[g] = first_row(j, g, next[g]);
@@ -834,17 +834,25 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     uint32_t uses[2] = {0, 0};  // segments that used O_0, O_1
     uint32_t states = 0;        // shared query tiles so far
     bool ok = true;
-    while (ok && next_segment<kQT, kRules>(a, blocks, walk, sg)) {
+    for (;;) {
+      // The segment, looked at here for what the tile loop needs and loaded
+      // again after it (a cache hit), so that a thread holding a whole score
+      // row holds little else: rules with the segment live across the loop
+      // spilled 440 bytes and took 2.4 us per pair of tiles, against 1.5.
+      Walk ahead_of = walk;
+      if (!next_segment<kQT, kRules>(a, blocks, ahead_of, sg)) break;
       const bool shared = kQT == 2 && shared_tile(a, sg);
       const int xq = shared ? 0 : x;  // query tile
       const int n_x = kQT == 1 ? sg.n : tiles_of<kRules>(a, sg, tpb, x);
-      const int n_other = kQT == 1 ? 0 : tiles_of<kRules>(a, sg, tpb, 1 - x);
-      const int tok = xq * tpt + tt;  // token within the block
-      const bool valid = tt < tpt && tok < sg.b.tokens;
       const int first_draft = sg.b.p;  // tree
       // rules: last key (but for the prefix) of the tile's first token, of this row
       const int min_limit = sg.b.p + sg.b.sub * tpb + xq * tpt;
-      const int limit = min_limit + (valid ? tt : 0);
+      const bool row_valid = tt < tpt && xq * tpt + tt < sg.b.tokens;
+      const int limit = min_limit + (row_valid ? tt : 0);
+      const int prefix = kRules != 0 ? sg.b.prefix : 0;
+      const TileWalk tiles = kRules != 0 ? sg.b.walk : TileWalk{0, 0};
+      // this group's tile j is tile first_tile + j * step of the block
+      const int first_tile = sg.tile0 + (shared ? x : 0), step = shared ? 2 : 1;
       float slope = 0.f;  // of this row's head, log2 units per key
       if constexpr (kBias) slope = a.rules.alibi_slopes[kvh * a.group + r % a.group] * kLog2e;
       // This row's ancestors (bit i: drafted key i), if the segment reaches
@@ -866,10 +874,10 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
           s_parents[x][i] = static_cast<uint8_t>(par < 0 ? 255 : par);
         }
         __syncwarp();
-        if (valid) {
+        if (row_valid) {
           // a parent is an earlier token: at most c steps (token 255 is
           // nobody's parent, so 255 can stand for the root)
-          for (int i = sg.b.sub * tpb + tok;;) {
+          for (int i = sg.b.sub * tpb + xq * tpt + tt;;) {
 #pragma unroll
             for (int w = 0; w < kMaskWords; ++w) anc[w] |= (i >> 5) == w ? 1u << (i & 31) : 0u;
             i = s_parents[x][i];
@@ -899,7 +907,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
           tmem_ld32_max(srow + 96, *reinterpret_cast<float(*)[32]>(&v[96]), mx3);
         }
         tmem_ld_wait();
-        const int key0 = tile_key<kRules>(sg.b, sg.tile0 + (shared ? 2 * j + x : j));
+        const int key0 = tile_key<kRules>(tiles, first_tile + j * step);
         // keys that some row may not see (uniform over the CTA or the group)
         const bool ahead = key0 + kN > (kRules == 0 ? first_draft : min_limit + 1);
         bool masked = ahead;
@@ -909,7 +917,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         if constexpr (kRules != 0) {
           const int window = a.rules.window;
           if (window > 0 && key0 < min_limit + tpt - window) masked = true;
-          if (key0 + kN <= sg.b.prefix) masked = false;
+          if (key0 + kN <= prefix) masked = false;
         }
         if constexpr (kCap || kBias) {
           const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
@@ -951,10 +959,14 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
             // column cc is seen if lo <= cc <= hi or cc < pre
             const int hi = limit - key0;
             const int lo = a.rules.window > 0 ? hi - a.rules.window + 1 : -key0;
-            const int pre = sg.b.prefix - key0;
+            const int pre = prefix - key0;
 #pragma unroll
-            for (int cc = 0; cc < kN; ++cc)
-              v[cc] = (cc >= lo && cc <= hi) || cc < pre ? v[cc] : -INFINITY;
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t seen = seen_bits(lo, hi, pre, w);
+#pragma unroll
+              for (int cc = 0; cc < 32; ++cc)
+                v[32 * w + cc] = (seen >> cc) & 1u ? v[32 * w + cc] : -INFINITY;
+            }
           }
           if (kRules == 0 && masked) {
             // word w: the visible ones of columns 32 w .. 32 w + 31
@@ -1063,6 +1075,10 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         mbar_arrive(bar(kBarPFull + buf));
       }
       if (!ok) break;
+      next_segment<kQT, kRules>(a, blocks, walk, sg);  // the same one
+      const int n_other = kQT == 1 ? 0 : tiles_of<kRules>(a, sg, tpb, 1 - x);
+      const int tok = xq * tpt + tt;  // token within the block
+      const bool valid = tt < tpt && tok < sg.b.tokens;
       pv_tiles += static_cast<uint32_t>(sg.n);
       if (n_x > 0) {
         if (!(ok = mbar_wait_warp(bar(kBarOFull + x), uses[x] & 1, abort))) break;

@@ -1025,8 +1025,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int lo = a.rules.window > 0 ? hi - a.rules.window + 1 : -key0;
               const int pre = d.prefix - key0;
 #pragma unroll
-              for (int cc = 0; cc < kN; ++cc)
-                v[cc] = (cc >= lo && cc <= hi) || cc < pre ? v[cc] : -INFINITY;
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t seen = seen_bits(lo, hi, pre, w);
+#pragma unroll
+                for (int cc = 0; cc < 32; ++cc)
+                  v[32 * w + cc] = (seen >> cc) & 1u ? v[32 * w + cc] : -INFINITY;
+              }
             }
           } else {
 #pragma unroll

@@ -92,6 +92,15 @@ __device__ __forceinline__ int rule_prefix(const int32_t *prefix_lens, int r, in
   return prefix_lens ? min(max(prefix_lens[r], 0), seq) : 0;
 }
 
+// Columns 32 w .. 32 w + 31 of a tile that a row sees, one bit each: those in
+// lo .. hi and those below pre.
+__device__ __forceinline__ uint32_t below_bits(int n) {  // the n lowest bits, 0 <= n clipped
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+__device__ __forceinline__ uint32_t seen_bits(int lo, int hi, int pre, int w) {
+  return (below_bits(hi + 1 - 32 * w) & ~below_bits(lo - 32 * w)) | below_bits(pre - 32 * w);
+}
+
 // The prefill softmax's part of the rules (a row of kRuleTile scores a thread).
 // A tile is near if a bound of each row's scores comes with the loads (the
 // largest absolute raw score of each 32 columns under a cap, the largest raw
