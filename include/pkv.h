@@ -375,10 +375,10 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
  * Keys that no query of the request's chunk sees are not read, nor are their
  * page_table entries. Hints and refusals as for pkv_paged_extend_attn; the
  * workspace is pkv_extend_mod_workspace_size(batch, total_q, Hq, Hkv, D,
- * max_seq_len_hint, max_total_keys_hint) bytes. A call with few queries (up to
- * 256 requests and 352 query blocks of 256 / (Hq / Hkv) tokens) reads K/V
- * straight from the pool; there a request past max_total_keys_hint is computed
- * all the same.
+ * max_seq_len_hint, max_total_keys_hint) bytes. A call whose queries are few
+ * for the keys they see reads K/V straight from the pool (a choice by these
+ * host-side sizes); there a request past max_total_keys_hint is computed all
+ * the same.
  */
 size_t pkv_extend_mod_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads,
                                      int32_t num_kv_heads, int32_t head_dim,

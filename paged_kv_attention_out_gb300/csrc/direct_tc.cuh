@@ -90,6 +90,13 @@ constexpr int producer_warps(int query_tiles, bool tma) {
   return tma || query_tiles == 2 ? 3 : 4;
 }
 
+// Registers per thread of the two-tile kernel's warpgroups: of 384 x 168 at
+// launch, the MMA and producer warps give up what the eight softmax warps take.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of the launch");
+static_assert(producer_warps(2, true) == 3 && producer_warps(2, false) == 3,
+              "three whole warpgroups");
+
 template <int D, int kQT>
 struct DirectSmem {
   static constexpr int kQBytes = kM * D * 2;   // one query tile
@@ -508,320 +515,326 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   Walk walk = s_walk;
   Segment sg;
 
-  if (warp >= kProducerWarp0) {
-    // ------------------------------------------------------------ producers
-    const int pw = warp - kProducerWarp0;
-    const int64_t row_elems = static_cast<int64_t>(a.hkv) * D;
-    const int64_t head_off = static_cast<int64_t>(kvh) * D;
-    // K/V that one block reads is read once: its lines go first (page size 64: 144.7 us against 150.2 with the default policy).
-    const uint64_t kv_policy = a.read_once ? l2_evict_first_policy() : l2_evict_normal_policy();
-    constexpr int kGroups = kTma ? 1 : kN / 32;  // boxes (keys) per lane and tile
-    constexpr int kChunks = D / 8;
-    constexpr int kKeysPerInstr = 32 / kChunks;
-    const int ch = lane % kChunks;
-    bool ok = true;
-    uint32_t u0 = 0;  // ring unit (K and V tiles) of the segment's first tile
-    uint32_t issued = 0;  // one past this warp's last unit
-    int segs = 0;
-    while (ok && next_segment<kQT, kRules>(a, blocks, walk, sg)) {
-      const int row = a.table_idx ? a.table_idx[sg.b.req] : sg.b.req;
-      const int32_t *pages = a.page_table + static_cast<int64_t>(row) * a.table_stride;
-      // This lane's boxes of tile j (kTma: box `lane` of the tile; otherwise
-      // one key of each 32): the page entry, loaded one of the warp's units
-      // ahead and looked at only when the tile's copies are issued, and the
-      // first pool row (-1 past the request or for a bad page).
-      const int box = kTma ? a.box : 1;
-      auto box_key = [&](int j, int g) -> int {
-        const int at = kTma ? lane * box : g * 32 + lane;
-        const int key = tile_key<kRules>(sg.b.walk, sg.tile0 + j) + at;
-        if (kRules != 0 && key >= sg.b.prefix && key + box <= sg.b.lo) return -1;  // seen by none
-        return at < kN && key < sg.b.seq ? key : -1;
-      };
-      auto load_entries = [&](int j, int (&e)[kGroups]) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const int key = box_key(j, g);
-          e[g] = key >= 0 ? __ldg(pages + key / a.page_size) : -1;
-        }
-      };
-      auto first_row = [&](int j, int g, int ent) -> long long {
-        const int key = box_key(j, g);
-        if (key < 0) return -1;
-        const long long s = static_cast<long long>(ent) * a.page_size + key % a.page_size;
-        if (ent < 0 || s + box > a.slots) {
-          flag_error(a.err, kErrPage);
-          return -1;
-        }
-        return s;
-      };
-      // this warp's units of the segment: first, first + kProducerWarps, ..
-      // (unit w holds K, or V if w is odd, of tile w / 2)
-      const uint32_t n_units = 2u * static_cast<uint32_t>(sg.n);
-      const uint32_t first =
-          (static_cast<uint32_t>(pw) + kProducerWarps - u0 % kProducerWarps) % kProducerWarps;
-      int next[kGroups];
-      if (first < n_units) load_entries(static_cast<int>(first >> 1), next);
-      if (pw == 0) {
-        if (segs > 0) ok = mbar_wait_warp(bar(kBarQEmpty), (segs - 1) & 1, abort);
-        if (ok && lane == 0) {
-          // only tiles that hold tokens are loaded (and computed)
-          const int nx = kQT == 2 && sg.b.tokens > tpt ? 2 : 1;
-          const uint32_t box_bytes = static_cast<uint32_t>(a.group * tpt) * 128u;
-          mbar_arrive_expect_tx(bar(kBarQFull), nx * kHalves * box_bytes);
-          for (int x = 0; x < nx; ++x)
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_3d(sbase + S::kQ + static_cast<uint32_t>(x * S::kQBytes + h * (kM * 128)),
-                          &q_map, h * 64, kvh * a.group, sg.b.t_base + x * tpt, bar(kBarQFull));
-        }
-        __syncwarp();
-        if (!ok) break;
-      }
-      ++segs;
-      for (uint32_t w = first; w < n_units; w += kProducerWarps) {
-        const int j = static_cast<int>(w >> 1), c = static_cast<int>(w & 1);
-        const uint32_t u = u0 + w;
-        const int key0 = tile_key<kRules>(sg.b.walk, sg.tile0 + j);
-        long long cur[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) cur[g] = first_row(j, g, next[g]);
-        if (w + kProducerWarps < n_units)
-          load_entries(static_cast<int>((w + kProducerWarps) >> 1), next);
-        const int st = static_cast<int>(u % kSlots);
-        if (u >= kSlots &&
-            !(ok = mbar_wait_warp(bar(kBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
-          break;
-        const uint32_t dst = sbase + S::kRing + st * S::kSlotBytes;
-        const __nv_bfloat16 *plane = (c ? a.v_plane : a.k_plane) + head_off;
-        if (kTma) {
-          // boxes of live keys by TMA; the box of the last key and those
-          // behind it (and bad pages) row by row, zeros where nothing is
-          const int b_lane = lane * box;
-          const bool in_tile = b_lane < kN;
-          // (under rules, boxes with rows that no token sees are not live)
-          const bool live = in_tile && cur[0] >= 0 && key0 + b_lane + box <= sg.b.seq &&
-                            (kRules == 0 || key0 + b_lane >= sg.b.lo ||
-                             key0 + b_lane + box <= sg.b.prefix);
-          const unsigned live_mask = __ballot_sync(0xffffffffu, live);
-          unsigned rest = __ballot_sync(0xffffffffu, in_tile && !live);
-          if (lane == 0)
-            mbar_expect_tx(bar(kBarFull + st),
-                           static_cast<uint32_t>(__popc(live_mask) * box * D * 2));
-          __syncwarp();
-          if (live) {
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              tma_load_2d_hint(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
-                               c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
-                               bar(kBarFull + st), kv_policy);
-          }
-          const bool copied = rest != 0;
-          while (rest) {
-            const int src = __ffs(rest) - 1;
-            rest &= rest - 1;
-            const long long s0 = __shfl_sync(0xffffffffu, cur[0], src);
-            for (int r = lane / kChunks; r < box; r += kKeysPerInstr) {
-              const int kk = src * box + r;
-              const bool in = s0 >= 0 && key0 + kk < sg.b.seq &&
-                              (kRules == 0 || key0 + kk >= sg.b.lo || key0 + kk < sg.b.prefix);
-              cp_async_16(dst + sw128_offset(kN, kk, ch * 8),
-                          in ? plane + (s0 + r) * row_elems + ch * 8 : plane, in ? 16 : 0);
-            }
-          }
-          if (copied) {  // landed, and visible to tcgen05.mma, before the arrival
-            cp_async_wait_all();
-            fence_async_shared();
-          }
-          mbar_arrive(bar(kBarFull + st));
-        } else {
-          // A lane knows the rows of four of the tile's keys; each copy takes
-          // its row's address from the lane that does. Eight addresses are
-          // exchanged before their copies: a copy keeps its place in the
-          // program, a shuffle between two would delay the second.
-          constexpr int kCopies = 32 / kKeysPerInstr;
-          constexpr int kAhead = 8;
+  if (warp >= kMmaWarp) {
+    // one warpgroup with two query tiles: the MMA warp and three producers
+    if constexpr (kQT == 2) warpgroup_registers_dec<kOtherRegs>();
+    if (warp >= kProducerWarp0) {
+      // ------------------------------------------------------------ producers
+      const int pw = warp - kProducerWarp0;
+      const int64_t row_elems = static_cast<int64_t>(a.hkv) * D;
+      const int64_t head_off = static_cast<int64_t>(kvh) * D;
+      // K/V that one block reads is read once: its lines go first (page size
+      // 64: 144.7 us against 150.2 with the default policy).
+      const uint64_t kv_policy = a.read_once ? l2_evict_first_policy() : l2_evict_normal_policy();
+      constexpr int kGroups = kTma ? 1 : kN / 32;  // boxes (keys) per lane and tile
+      constexpr int kChunks = D / 8;
+      constexpr int kKeysPerInstr = 32 / kChunks;
+      const int ch = lane % kChunks;
+      bool ok = true;
+      uint32_t u0 = 0;  // ring unit (K and V tiles) of the segment's first tile
+      uint32_t issued = 0;  // one past this warp's last unit
+      int segs = 0;
+      while (ok && next_segment<kQT, kRules>(a, blocks, walk, sg)) {
+        const int row = a.table_idx ? a.table_idx[sg.b.req] : sg.b.req;
+        const int32_t *pages = a.page_table + static_cast<int64_t>(row) * a.table_stride;
+        // This lane's boxes of tile j (kTma: box `lane` of the tile; otherwise
+        // one key of each 32): the page entry, loaded one of the warp's units
+        // ahead and looked at only when the tile's copies are issued, and the
+        // first pool row (-1 past the request or for a bad page).
+        const int box = kTma ? a.box : 1;
+        auto box_key = [&](int j, int g) -> int {
+          const int at = kTma ? lane * box : g * 32 + lane;
+          const int key = tile_key<kRules>(sg.b.walk, sg.tile0 + j) + at;
+          if (kRules != 0 && key >= sg.b.prefix && key + box <= sg.b.lo) return -1;  // seen by none
+          return at < kN && key < sg.b.seq ? key : -1;
+        };
+        auto load_entries = [&](int j, int (&e)[kGroups]) {
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            const bool in = cur[g] >= 0;
-            const unsigned mask = __ballot_sync(0xffffffffu, in) >> (lane / kChunks);
-            const uint64_t row_at =
-                reinterpret_cast<uint64_t>(in ? plane + cur[g] * row_elems : plane);
+            const int key = box_key(j, g);
+            e[g] = key >= 0 ? __ldg(pages + key / a.page_size) : -1;
+          }
+        };
+        auto first_row = [&](int j, int g, int ent) -> long long {
+          const int key = box_key(j, g);
+          if (key < 0) return -1;
+          const long long s = static_cast<long long>(ent) * a.page_size + key % a.page_size;
+          if (ent < 0 || s + box > a.slots) {
+            flag_error(a.err, kErrPage);
+            return -1;
+          }
+          return s;
+        };
+        // this warp's units of the segment: first, first + kProducerWarps, ..
+        // (unit w holds K, or V if w is odd, of tile w / 2)
+        const uint32_t n_units = 2u * static_cast<uint32_t>(sg.n);
+        const uint32_t first =
+            (static_cast<uint32_t>(pw) + kProducerWarps - u0 % kProducerWarps) % kProducerWarps;
+        int next[kGroups];
+        if (first < n_units) load_entries(static_cast<int>(first >> 1), next);
+        if (pw == 0) {
+          if (segs > 0) ok = mbar_wait_warp(bar(kBarQEmpty), (segs - 1) & 1, abort);
+          if (ok && lane == 0) {
+            // only tiles that hold tokens are loaded (and computed)
+            const int nx = kQT == 2 && sg.b.tokens > tpt ? 2 : 1;
+            const uint32_t box_bytes = static_cast<uint32_t>(a.group * tpt) * 128u;
+            mbar_arrive_expect_tx(bar(kBarQFull), nx * kHalves * box_bytes);
+            for (int x = 0; x < nx; ++x)
 #pragma unroll
-            for (int i0 = 0; i0 < kCopies; i0 += kAhead) {
-              uint64_t src[kAhead];
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_3d(sbase + S::kQ + static_cast<uint32_t>(x * S::kQBytes + h * (kM * 128)),
+                            &q_map, h * 64, kvh * a.group, sg.b.t_base + x * tpt, bar(kBarQFull));
+          }
+          __syncwarp();
+          if (!ok) break;
+        }
+        ++segs;
+        for (uint32_t w = first; w < n_units; w += kProducerWarps) {
+          const int j = static_cast<int>(w >> 1), c = static_cast<int>(w & 1);
+          const uint32_t u = u0 + w;
+          const int key0 = tile_key<kRules>(sg.b.walk, sg.tile0 + j);
+          long long cur[kGroups];
 #pragma unroll
-              for (int i = 0; i < kAhead; ++i)
-                src[i] = __shfl_sync(0xffffffffu, row_at,
-                                     (i0 + i) * kKeysPerInstr + lane / kChunks) +
-                         ch * 16;
+          for (int g = 0; g < kGroups; ++g) cur[g] = first_row(j, g, next[g]);
+          if (w + kProducerWarps < n_units)
+            load_entries(static_cast<int>((w + kProducerWarps) >> 1), next);
+          const int st = static_cast<int>(u % kSlots);
+          if (u >= kSlots &&
+              !(ok = mbar_wait_warp(bar(kBarEmpty + st), ((u / kSlots) - 1) & 1, abort)))
+            break;
+          const uint32_t dst = sbase + S::kRing + st * S::kSlotBytes;
+          const __nv_bfloat16 *plane = (c ? a.v_plane : a.k_plane) + head_off;
+          if (kTma) {
+            // boxes of live keys by TMA; the box of the last key and those
+            // behind it (and bad pages) row by row, zeros where nothing is
+            const int b_lane = lane * box;
+            const bool in_tile = b_lane < kN;
+            // (under rules, boxes with rows that no token sees are not live)
+            const bool live = in_tile && cur[0] >= 0 && key0 + b_lane + box <= sg.b.seq &&
+                              (kRules == 0 || key0 + b_lane >= sg.b.lo ||
+                               key0 + b_lane + box <= sg.b.prefix);
+            const unsigned live_mask = __ballot_sync(0xffffffffu, live);
+            unsigned rest = __ballot_sync(0xffffffffu, in_tile && !live);
+            if (lane == 0)
+              mbar_expect_tx(bar(kBarFull + st),
+                             static_cast<uint32_t>(__popc(live_mask) * box * D * 2));
+            __syncwarp();
+            if (live) {
 #pragma unroll
-              for (int i = 0; i < kAhead; ++i)
-                cp_async_16_hint(
-                    dst + sw128_offset(kN, g * 32 + (i0 + i) * kKeysPerInstr + lane / kChunks,
-                                       ch * 8),
-                    reinterpret_cast<const void *>(src[i]),
-                    (mask >> ((i0 + i) * kKeysPerInstr)) & 1u ? 16 : 0, kv_policy);
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_2d_hint(dst + static_cast<uint32_t>(h * (kN * 128) + b_lane * 128),
+                                 c ? &v_map : &k_map, kvh * D + h * 64, static_cast<int>(cur[0]),
+                                 bar(kBarFull + st), kv_policy);
+            }
+            const bool copied = rest != 0;
+            while (rest) {
+              const int src = __ffs(rest) - 1;
+              rest &= rest - 1;
+              const long long s0 = __shfl_sync(0xffffffffu, cur[0], src);
+              for (int r = lane / kChunks; r < box; r += kKeysPerInstr) {
+                const int kk = src * box + r;
+                const bool in = s0 >= 0 && key0 + kk < sg.b.seq &&
+                                (kRules == 0 || key0 + kk >= sg.b.lo || key0 + kk < sg.b.prefix);
+                cp_async_16(dst + sw128_offset(kN, kk, ch * 8),
+                            in ? plane + (s0 + r) * row_elems + ch * 8 : plane, in ? 16 : 0);
+              }
+            }
+            if (copied) {  // landed, and visible to tcgen05.mma, before the arrival
+              cp_async_wait_all();
+              fence_async_shared();
+            }
+            mbar_arrive(bar(kBarFull + st));
+          } else {
+            // A lane knows the rows of four of the tile's keys; each copy takes
+            // its row's address from the lane that does. Eight addresses are
+            // exchanged before their copies: a copy keeps its place in the
+            // program, a shuffle between two would delay the second.
+            constexpr int kCopies = 32 / kKeysPerInstr;
+            constexpr int kAhead = 8;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const bool in = cur[g] >= 0;
+              const unsigned mask = __ballot_sync(0xffffffffu, in) >> (lane / kChunks);
+              const uint64_t row_at =
+                  reinterpret_cast<uint64_t>(in ? plane + cur[g] * row_elems : plane);
+#pragma unroll
+              for (int i0 = 0; i0 < kCopies; i0 += kAhead) {
+                uint64_t src[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                  src[i] = __shfl_sync(0xffffffffu, row_at,
+                                       (i0 + i) * kKeysPerInstr + lane / kChunks) +
+                           ch * 16;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                  cp_async_16_hint(
+                      dst + sw128_offset(kN, g * 32 + (i0 + i) * kKeysPerInstr + lane / kChunks,
+                                         ch * 8),
+                      reinterpret_cast<const void *>(src[i]),
+                      (mask >> ((i0 + i) * kKeysPerInstr)) & 1u ? 16 : 0, kv_policy);
+              }
             }
           }
+          if (!kTma) cp_async_mbar_arrive(bar(kBarFull + st));
+          issued = u + 1;
         }
-        if (!kTma) cp_async_mbar_arrive(bar(kBarFull + st));
-        issued = u + 1;
+        u0 += n_units;
       }
-      u0 += n_units;
-    }
-    if (!ok) *abort = 1;
-    cp_async_wait_all();
-    if (*abort && lane == 0) {
-      // every TMA copy this warp issued lands before the CTA can exit
-      int never = 0;
-      if (pw == 0 && segs > 0) mbar_wait(bar(kBarQFull), (segs - 1) & 1, &never);
-      if (kTma)
-        for (uint32_t t = issued > kSlots ? issued - kSlots : 0; t < issued; ++t)
-          if (t % kProducerWarps == static_cast<uint32_t>(pw))
-            mbar_wait(bar(kBarFull + t % kSlots), (t / kSlots) & 1, &never);
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    const bool issuer = elect_one();
-    constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
-    constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
-    const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
-    const uint64_t dk0 = umma_desc_sw128(sbase + S::kRing, 16, 1024);
-    const uint64_t dv0 = umma_desc_sw128(sbase + S::kRing, kN * 128, 1024);
-    auto kstep = [](int ks) -> uint64_t {
-      return static_cast<uint64_t>(((ks >> 2) * (kN * 128) + (ks & 3) * 32) >> 4);
-    };
-    auto slot_step = [](uint32_t u) -> uint64_t {
-      return static_cast<uint64_t>((u % kSlots) * (S::kSlotBytes >> 4));
-    };
-    auto qk = [&](int x, int buf, uint32_t u) {  // scores of query tile x, K in unit u
-      const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
-      const uint64_t dk = dk0 + slot_step(u);
-      if (issuer) {
+      if (!ok) *abort = 1;
+      cp_async_wait_all();
+      if (*abort && lane == 0) {
+        // every TMA copy this warp issued lands before the CTA can exit
+        int never = 0;
+        if (pw == 0 && segs > 0) mbar_wait(bar(kBarQFull), (segs - 1) & 1, &never);
+        if (kTma)
+          for (uint32_t t = issued > kSlots ? issued - kSlots : 0; t < issued; ++t)
+            if (t % kProducerWarps == static_cast<uint32_t>(pw))
+              mbar_wait(bar(kBarFull + t % kSlots), (t / kSlots) & 1, &never);
+      }
+    } else {
+      // ------------------------------------------------------------ MMA issuer
+      const bool issuer = elect_one();
+      constexpr uint32_t idesc_qk = umma_idesc_bf16(kM, kN, 0, 0);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(kM, D, 0, 1);
+      const uint64_t dq0 = umma_desc_sw128(sbase + S::kQ, 16, 1024);
+      const uint64_t dk0 = umma_desc_sw128(sbase + S::kRing, 16, 1024);
+      const uint64_t dv0 = umma_desc_sw128(sbase + S::kRing, kN * 128, 1024);
+      auto kstep = [](int ks) -> uint64_t {
+        return static_cast<uint64_t>(((ks >> 2) * (kN * 128) + (ks & 3) * 32) >> 4);
+      };
+      auto slot_step = [](uint32_t u) -> uint64_t {
+        return static_cast<uint64_t>((u % kSlots) * (S::kSlotBytes >> 4));
+      };
+      auto qk = [&](int x, int buf, uint32_t u) {  // scores of query tile x, K in unit u
+        const uint64_t dq = dq0 + static_cast<uint64_t>((x * S::kQBytes) >> 4);
+        const uint64_t dk = dk0 + slot_step(u);
+        if (issuer) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16_ss(tmem + kTmemS + buf * kN, dq + kstep(ks), dk + kstep(ks), idesc_qk,
-                       ks > 0 ? 1u : 0u);
-        umma_commit(bar(kBarSFull + buf));
-      }
-    };
-    auto pv = [&](int x, int buf, uint32_t u, bool first) {  // O_x (+)= P V, V in unit u
-      const uint64_t dv = dv0 + slot_step(u);
-      if (issuer) {
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16_ss(tmem + kTmemS + buf * kN, dq + kstep(ks), dk + kstep(ks), idesc_qk,
+                         ks > 0 ? 1u : 0u);
+          umma_commit(bar(kBarSFull + buf));
+        }
+      };
+      auto pv = [&](int x, int buf, uint32_t u, bool first) {  // O_x (+)= P V, V in unit u
+        const uint64_t dv = dv0 + slot_step(u);
+        if (issuer) {
 #pragma unroll
-        for (int ks = 0; ks < kN / 16; ++ks)
-          umma_bf16_ts(tmem + kTmemO + x * kN, tmem + kTmemS + buf * kN + ks * 8,
-                       dv + ks * (2048 >> 4), idesc_pv, (!first || ks > 0) ? 1u : 0u);
-      }
-    };
-    auto commit = [&](int i) {
-      if (issuer) umma_commit(bar(i));
-    };
-    auto wait_unit = [&](uint32_t u) {
-      const bool r = mbar_wait_uniform(bar(kBarFull + u % kSlots), (u / kSlots) & 1, abort);
-      if (!kTma) fence_async_shared();  // cp.async wrote it, tcgen05.mma reads it
-      tc_fence_after_sync();
-      return r;
-    };
-    auto free_unit = [&](uint32_t u) { commit(kBarEmpty + static_cast<int>(u % kSlots)); };
-    uint32_t u0 = 0;                // ring unit of the segment's first K tile
-    uint32_t np0 = 0, np1 = 0;      // P tiles taken from score buffers 0 and 1
-    uint32_t uses0 = 0, uses1 = 0;  // segments that used O_0, O_1
-    int segs = 0;
-    bool ok = true;
-    while (ok && next_segment<kQT, kRules>(a, blocks, walk, sg)) {
-      const int n = sg.n;
-      if (!(ok = mbar_wait_uniform(bar(kBarQFull), segs & 1, abort))) break;
-      ++segs;
-      // One query tile: key tiles alternate between the score buffers, and
-      // (two-tile kernel) between the softmax groups and their O.
-      const bool alternate = kQT == 1 || shared_tile(a, sg);
-      if (alternate) {
-        for (int j = 0; ok && j < 2 && j < n; ++j) {
-          if (!(ok = wait_unit(u0 + 2 * j))) break;
-          qk(0, j, u0 + 2 * j);
-          free_unit(u0 + 2 * j);
+          for (int ks = 0; ks < kN / 16; ++ks)
+            umma_bf16_ts(tmem + kTmemO + x * kN, tmem + kTmemS + buf * kN + ks * 8,
+                         dv + ks * (2048 >> 4), idesc_pv, (!first || ks > 0) ? 1u : 0u);
         }
-        if (n <= 2 && ok) commit(kBarQEmpty);
-        for (int j = 0; ok && j < n; ++j) {
-          const int buf = j & 1;
-          const int x = kQT == 2 ? buf : 0;
-          uint32_t &np = buf ? np1 : np0;
-          const uint32_t uses = x ? uses1 : uses0;
-          const bool first = j <= x;  // of O_x
-          if (first && uses > 0 &&
-              !(ok = mbar_wait_uniform(bar(kBarOEmpty + x), (uses - 1) & 1, abort)))
-            break;
-          if (!(ok = mbar_wait_uniform(bar(kBarPFull + buf), np & 1, abort) &&
-                     wait_unit(u0 + 2 * j + 1)))
-            break;
-          ++np;
-          pv(x, buf, u0 + 2 * j + 1, first);
-          free_unit(u0 + 2 * j + 1);
-          if (kQT == 1) commit(kBarPvDone);
-          if (kQT == 2 && j + 2 >= n) commit(kBarOFull + x);
-          if (j + 2 < n) {
-            if (!(ok = wait_unit(u0 + 2 * (j + 2)))) break;
-            qk(0, buf, u0 + 2 * (j + 2));
-            free_unit(u0 + 2 * (j + 2));
-            if (j + 3 == n) commit(kBarQEmpty);
+      };
+      auto commit = [&](int i) {
+        if (issuer) umma_commit(bar(i));
+      };
+      auto wait_unit = [&](uint32_t u) {
+        const bool r = mbar_wait_uniform(bar(kBarFull + u % kSlots), (u / kSlots) & 1, abort);
+        if (!kTma) fence_async_shared();  // cp.async wrote it, tcgen05.mma reads it
+        tc_fence_after_sync();
+        return r;
+      };
+      auto free_unit = [&](uint32_t u) { commit(kBarEmpty + static_cast<int>(u % kSlots)); };
+      uint32_t u0 = 0;                // ring unit of the segment's first K tile
+      uint32_t np0 = 0, np1 = 0;      // P tiles taken from score buffers 0 and 1
+      uint32_t uses0 = 0, uses1 = 0;  // segments that used O_0, O_1
+      int segs = 0;
+      bool ok = true;
+      while (ok && next_segment<kQT, kRules>(a, blocks, walk, sg)) {
+        const int n = sg.n;
+        if (!(ok = mbar_wait_uniform(bar(kBarQFull), segs & 1, abort))) break;
+        ++segs;
+        // One query tile: key tiles alternate between the score buffers, and
+        // (two-tile kernel) between the softmax groups and their O.
+        const bool alternate = kQT == 1 || shared_tile(a, sg);
+        if (alternate) {
+          for (int j = 0; ok && j < 2 && j < n; ++j) {
+            if (!(ok = wait_unit(u0 + 2 * j))) break;
+            qk(0, j, u0 + 2 * j);
+            free_unit(u0 + 2 * j);
           }
-        }
-        if (kQT == 1 && ok) commit(kBarOFull);
-        ++uses0;
-        if (kQT == 2) ++uses1;
-      } else {
-        const int n0 = tiles_of<kRules>(a, sg, tpb, 0), n1 = tiles_of<kRules>(a, sg, tpb, 1);
-        // score tile j of both query tiles, for those that walk it
-        if (!(ok = wait_unit(u0))) break;
-        if (n0 > 0) qk(0, 0, u0);
-        if (n1 > 0) qk(1, 1, u0);
-        free_unit(u0);
-        if (n == 1) commit(kBarQEmpty);
-        for (int j = 0; ok && j < n; ++j) {
-          const uint32_t uk = u0 + 2 * (j + 1), uv = u0 + 2 * j + 1;
-          const bool next = j + 1 < n;
-          if (!(ok = wait_unit(uv))) break;
-          if (j < n0) {
-            if (j == 0 && uses0 > 0 &&
-                !(ok = mbar_wait_uniform(bar(kBarOEmpty), (uses0 - 1) & 1, abort)))
+          if (n <= 2 && ok) commit(kBarQEmpty);
+          for (int j = 0; ok && j < n; ++j) {
+            const int buf = j & 1;
+            const int x = kQT == 2 ? buf : 0;
+            uint32_t &np = buf ? np1 : np0;
+            const uint32_t uses = x ? uses1 : uses0;
+            const bool first = j <= x;  // of O_x
+            if (first && uses > 0 &&
+                !(ok = mbar_wait_uniform(bar(kBarOEmpty + x), (uses - 1) & 1, abort)))
               break;
-            if (!(ok = mbar_wait_uniform(bar(kBarPFull), np0 & 1, abort))) break;
-            tc_fence_after_sync();
-            ++np0;
-            pv(0, 0, uv, j == 0);
-            if (j == n0 - 1) commit(kBarOFull);
-          }
-          if (next && !(ok = wait_unit(uk))) break;
-          if (next && j + 1 < n0) qk(0, 0, uk);
-          if (j < n1) {
-            if (j == 0 && uses1 > 0 &&
-                !(ok = mbar_wait_uniform(bar(kBarOEmpty + 1), (uses1 - 1) & 1, abort)))
+            if (!(ok = mbar_wait_uniform(bar(kBarPFull + buf), np & 1, abort) &&
+                       wait_unit(u0 + 2 * j + 1)))
               break;
-            if (!(ok = mbar_wait_uniform(bar(kBarPFull + 1), np1 & 1, abort))) break;
-            tc_fence_after_sync();
-            ++np1;
-            pv(1, 1, uv, j == 0);
-            if (j == n1 - 1) commit(kBarOFull + 1);
+            ++np;
+            pv(x, buf, u0 + 2 * j + 1, first);
+            free_unit(u0 + 2 * j + 1);
+            if (kQT == 1) commit(kBarPvDone);
+            if (kQT == 2 && j + 2 >= n) commit(kBarOFull + x);
+            if (j + 2 < n) {
+              if (!(ok = wait_unit(u0 + 2 * (j + 2)))) break;
+              qk(0, buf, u0 + 2 * (j + 2));
+              free_unit(u0 + 2 * (j + 2));
+              if (j + 3 == n) commit(kBarQEmpty);
+            }
           }
-          free_unit(uv);
-          if (next) {
-            if (j + 1 < n1) qk(1, 1, uk);
-            free_unit(uk);
+          if (kQT == 1 && ok) commit(kBarOFull);
+          ++uses0;
+          if (kQT == 2) ++uses1;
+        } else {
+          const int n0 = tiles_of<kRules>(a, sg, tpb, 0), n1 = tiles_of<kRules>(a, sg, tpb, 1);
+          // score tile j of both query tiles, for those that walk it
+          if (!(ok = wait_unit(u0))) break;
+          if (n0 > 0) qk(0, 0, u0);
+          if (n1 > 0) qk(1, 1, u0);
+          free_unit(u0);
+          if (n == 1) commit(kBarQEmpty);
+          for (int j = 0; ok && j < n; ++j) {
+            const uint32_t uk = u0 + 2 * (j + 1), uv = u0 + 2 * j + 1;
+            const bool next = j + 1 < n;
+            if (!(ok = wait_unit(uv))) break;
+            if (j < n0) {
+              if (j == 0 && uses0 > 0 &&
+                  !(ok = mbar_wait_uniform(bar(kBarOEmpty), (uses0 - 1) & 1, abort)))
+                break;
+              if (!(ok = mbar_wait_uniform(bar(kBarPFull), np0 & 1, abort))) break;
+              tc_fence_after_sync();
+              ++np0;
+              pv(0, 0, uv, j == 0);
+              if (j == n0 - 1) commit(kBarOFull);
+            }
+            if (next && !(ok = wait_unit(uk))) break;
+            if (next && j + 1 < n0) qk(0, 0, uk);
+            if (j < n1) {
+              if (j == 0 && uses1 > 0 &&
+                  !(ok = mbar_wait_uniform(bar(kBarOEmpty + 1), (uses1 - 1) & 1, abort)))
+                break;
+              if (!(ok = mbar_wait_uniform(bar(kBarPFull + 1), np1 & 1, abort))) break;
+              tc_fence_after_sync();
+              ++np1;
+              pv(1, 1, uv, j == 0);
+              if (j == n1 - 1) commit(kBarOFull + 1);
+            }
+            free_unit(uv);
+            if (next) {
+              if (j + 1 < n1) qk(1, 1, uk);
+              free_unit(uk);
+            }
+            if (j + 2 == n) commit(kBarQEmpty);
           }
-          if (j + 2 == n) commit(kBarQEmpty);
+          if (n0 > 0) ++uses0;
+          if (n1 > 0) ++uses1;
         }
-        if (n0 > 0) ++uses0;
-        if (n1 > 0) ++uses1;
+        u0 += 2 * static_cast<uint32_t>(n);
       }
-      u0 += 2 * static_cast<uint32_t>(n);
-    }
-    if (!ok) {
-      *abort = 1;
-      flag_error(a.err, kErrTimeout);
+      if (!ok) {
+        *abort = 1;
+        flag_error(a.err, kErrTimeout);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (kQT == 2) warpgroup_registers_inc<kSoftmaxRegs>();
     const int quarter = warp & 3;
     const int x = kQT == 2 ? warp >> 2 : 0;
     const int r = quarter * 32 + lane;  // row of the query tile == TMEM lane
@@ -1041,7 +1054,8 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         if constexpr (kCap || kBias) {
           if (near)
             exponentials([&](int cc, float &y0, float &y1) {
-              near_pair<kCap, kBias>(v[cc], v[cc + 1], cc, a.scale_log2, slope, nm, a.rules, y0, y1);
+              near_pair<kCap, kBias>(v[cc], v[cc + 1], cc, a.scale_log2, slope, nm, a.rules, y0,
+                                     y1);
             });
           else
             exponentials([&](int cc, float &y0, float &y1) {
@@ -1283,6 +1297,15 @@ template <int D, int kQT, bool kTma, int kRules>
 cudaError_t launch(const DirectArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
                    const CUtensorMap &qm, cudaStream_t stream) {
   using S = DirectSmem<D, kQT>;
+  if constexpr (kQT == 2) {
+    // the register split waits forever if the launch has fewer than it hands out
+    static const bool enough = [] {
+      cudaFuncAttributes at{};
+      return cudaFuncGetAttributes(&at, direct_kernel<D, kQT, kTma, kRules>) == cudaSuccess &&
+             3 * at.numRegs >= 2 * kSoftmaxRegs + kOtherRegs;
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+  }
   cudaError_t e = cudaFuncSetAttribute(direct_kernel<D, kQT, kTma, kRules>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
   if (e != cudaSuccess) return e;

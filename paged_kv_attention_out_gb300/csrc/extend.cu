@@ -1089,7 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kCap || kBias) {
           if (near) {
             exponentials([&](int cc, float &y0, float &y1) {
-              near_pair<kCap, kBias>(v[cc], v[cc + 1], cc, a.scale_log2, slope, nm, a.rules, y0, y1);
+              near_pair<kCap, kBias>(v[cc], v[cc + 1], cc, a.scale_log2, slope, nm, a.rules, y0,
+                                     y1);
             });
           } else {
             exponentials([&](int cc, float &y0, float &y1) {

@@ -3,16 +3,38 @@
 //
 // Against the gather and attention of extend.cu: no copy of the keys, and the
 // work is shared out by key tiles instead of whole blocks, so a call with fewer
-// blocks than SMs, or with a long prefix and a short chunk, fills the GPU.
+// blocks than SMs, or with a long prefix and a short chunk, fills the GPU. With
+// enough blocks the gathered form is the faster one: its K/V tiles come by
+// large boxes, and its softmax keeps less state.
 #include "extend_direct.cuh"
 
 namespace pkv {
 
+// Which of the two forms takes less time, in microseconds, by their measured
+// parts: the longest block (T key tiles) bounds the gathered form while there
+// are fewer (block, kv head) pairs N than SMs, the direct one shares N T tiles
+// out evenly, at more per tile and with a merge. (D = 128, page size 16, cap 50
+// and window 4096, direct / gathered: 4 requests of one token over up to 2000
+// keys 25 / 34; 2 of 64 over up to 8000 keys 37 / 65; 2 of up to 300 over up to
+// 1500 keys 36 / 32; 1 of 1000 over 3000 keys 62 / 49; 4 of up to 2048 over up
+// to 8192 keys 258 / 190.)
+static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
+  const double gathered = 12.0 + 1.5 * tiles * ((pairs + sms - 1) / sms);
+  const double direct = 24.0 + 2.1 * static_cast<double>(pairs) * tiles / sms;
+  return direct < gathered;
+}
+
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
-                        int32_t max_seq, int32_t sm_count, DirectPlan *plan) {
+                        int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan) {
   const int32_t tpb = 2 * (direct::kM / (hq / hkv));
   const int64_t blocks = (static_cast<int64_t>(total_q) + tpb - 1) / tpb + batch;
   if (batch > direct::kMaxRuleRequests || blocks > direct::kMaxRuleBlocks) return false;
+  // key tiles of a block: all up to the longest request's, or the window's
+  int64_t tiles = (static_cast<int64_t>(max_seq) + direct::kN - 1) / direct::kN;
+  if (window > 0)
+    tiles = std::min<int64_t>(tiles, (static_cast<int64_t>(window) + tpb) / direct::kN + 2);
+  const int64_t busy = std::max<int64_t>(batch, (static_cast<int64_t>(total_q) + tpb - 1) / tpb);
+  if (!direct_is_faster(busy * hkv, tiles, sm_count > 0 ? sm_count : 1)) return false;
   *plan = direct::plan(static_cast<int32_t>(blocks), 2, hkv, d, max_seq, sm_count);
   return true;
 }

@@ -542,8 +542,10 @@ size_t pkv_extend_mod_workspace_size(int32_t batch, int32_t total_q, int32_t num
   DevInfo *d = nullptr;
   if (device_info(&d) != PKV_OK) return 0;
   pkv::DirectPlan plan;
+  // (the size of the direct form for any window: it depends on the bound of
+  // the lengths alone)
   if (!pkv::extend_direct_plan(batch, total_q, num_q_heads, num_kv_heads, head_dim,
-                               max_seq_len_hint, d->sm_count, &plan))
+                               max_seq_len_hint, 0, d->sm_count, &plan))
     return gathered;
   return plan.workspace_bytes > gathered ? plan.workspace_bytes : gathered;
 }
@@ -609,7 +611,8 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
     if ((s = device_info(&d)) != PKV_OK) return s;
     pkv::DirectPlan plan;
     if (pkv::extend_direct_plan(batch, total_q, num_q_heads, g.hkv, g.d,
-                                static_cast<int32_t>(cap), d->sm_count, &plan)) {
+                                static_cast<int32_t>(cap),
+                                rules.prefix_lens ? 0 : rules.window, d->sm_count, &plan)) {
       if ((s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)
         return s;
       const cudaError_t e = pkv::launch_extend_direct(

@@ -173,10 +173,11 @@ cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const i
                         const DirectPlan &plan, void *workspace, unsigned *err,
                         cudaStream_t stream);
 
-// Extend under score rules with few query blocks (extend_direct.cu); false:
-// more blocks or requests than it takes.
+// Extend under score rules with few query blocks (extend_direct.cu); window: the
+// rules' (0 for none, or where a prefix adds to it). false: more blocks or
+// requests than it takes, or the form of extend.cu is faster.
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
-                        int32_t max_seq, int32_t sm_count, DirectPlan *plan);
+                        int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan);
 cudaError_t launch_extend_direct(const PoolGeom &g, int32_t layer, const void *q,
                                  const int32_t *qo_indptr, void *o, float *lse,
                                  const int32_t *page_table, int64_t table_stride,

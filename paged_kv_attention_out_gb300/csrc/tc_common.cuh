@@ -380,6 +380,18 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return __all_sync(0xffffffffu, ok);
 }
 
+// Registers per thread of the calling warpgroup (all four warps, the same
+// instruction) from here on; what one gives up another may take, up to the
+// block's registers at launch.
+template <int N>
+__device__ __forceinline__ void warpgroup_registers_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void warpgroup_registers_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Barrier among `count` threads (a multiple of 32) of the CTA on hardware
 // barrier `id` (1 .. 15; 0 is the one __syncthreads uses).
 __device__ __forceinline__ void named_barrier_sync(int id, int count) {

@@ -181,6 +181,52 @@ def test_extend_tables_are_checked_in_both_forms():
         flagged(PAGE, [0, 2], set_("page_table", (1, 18), case.NP + 3))
 
 
+LONG_RULES = [
+    dict(cap=30.0), dict(cap=2.0), dict(alibi=True), dict(window=2000), dict(prefix=[40, 2700]),
+    dict(window=64, prefix=[5, 2900, 130]), dict(cap=1.0, alibi=True), dict(cap=50.0, window=2500),
+    dict(alibi=True, window=90, prefix=[17]), dict(cap=20.0, alibi=True, window=129, prefix=[128, 1000]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", LONG_RULES, ids=str)
+@pytest.mark.parametrize("D,P,Hq,Hkv", [(64, 1, 4, 2), (128, 16, 8, 2), (128, 7, 7, 1),
+                                        (64, 64, 16, 1)])
+def test_few_queries_over_long_rows(rule, D, P, Hq, Hkv):
+    """The direct form: blocks of one and of two query tiles, shared by groups of CTAs."""
+    case = W.random_case(21, kind="extend", seq_lens=[3000, 2817, 1], chunk_lens=[37, 1, 1], Hq=Hq,
+                         Hkv=Hkv, D=D, P=P, use_table_idx=True)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+@pytest.mark.parametrize("rule", [dict(cap=3.0), dict(cap=3.0, alibi=True), dict(prefix=[900])],
+                         ids=str)
+def test_scales_of_few_queries_over_long_rows(scale, rule):
+    case = W.random_case(22, kind="extend", seq_lens=[3000, 500], chunk_lens=[9, 40], Hq=4, Hkv=2,
+                         D=64, P=16)
+    mod_check(Rules(case, **rule), scale=scale)
+
+
+@pytest.mark.gpu
+def test_pages_outside_the_rules_are_never_read_over_long_rows():
+    case = W.random_case(23, kind="extend", seq_lens=[4000, 3500], chunk_lens=[40, 13], Hq=8, Hkv=2,
+                         D=64, P=16)
+    rules = Rules(case, window=1900, prefix=[20, 0], cap=10.0)
+
+    def free(pool, t):
+        for r in range(case.B):
+            first_seen = rules.first(r) - 1899
+            gone = np.arange(int(rules.prefix[r]), first_seen)
+            slots = torch.as_tensor(np.asarray(case.token_slots[r])[gone].astype(np.int64)).cuda()
+            pool[:, 0].flatten(1, 2)[:, slots] = float("nan")
+            for pg in range(int(rules.prefix[r] + 15) // 16, first_seen // 16):
+                t["page_table"][r, pg] = -7 - pg
+
+    mod_check(rules, before=free)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("P", [1, 16])
 @pytest.mark.parametrize("rule", [dict(cap=30.0), dict(window=1000, prefix=[200]),
@@ -286,8 +332,8 @@ def test_empty_rows_and_prefix_clipping():
 def test_a_workspace_of_any_contents():
     """The block table's entries past the call's last block must not be taken for blocks: here
     they would name token 0 (and its group's states), which a later block would overwrite."""
-    case = W.random_case(20, kind="extend", seq_lens=[900, 300, 700, 5], chunk_lens=[70, 1, 33, 5],
-                         Hq=8, Hkv=2, D=64, P=16)
+    case = W.random_case(20, kind="extend", seq_lens=[3900, 300, 700, 5],
+                         chunk_lens=[70, 1, 33, 5], Hq=8, Hkv=2, D=64, P=16)
     mod_check(Rules(case, cap=20.0), stale=[0, 0, 0, 1])
 
 
