@@ -161,6 +161,15 @@ def _contig(t: torch.Tensor, name: str):
 
 # The calls below are launch-bound at decode sizes, so each tensor is checked by
 # one short expression; what is wrong is found out only when something is.
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its lazy set-up
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _handle(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
 def _refuse(t, dtype, ndim: int, dev: int, name: str):
     _want(t, dtype, name, ndim)
     if t.get_device() != dev:
@@ -178,11 +187,11 @@ def _arg(t, dtype, ndim: int, dev: int, name: str) -> int:
 
 def _rows_arg(t, shape, dev: int, name: str) -> tuple[int, int]:
     """(address, elements between rows) of a bf16 [N, heads, D] tensor with contiguous rows."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
-        _want(t, torch.bfloat16, name, 3)
+    if t.dtype is not _bf16 or t.get_device() != dev or t.shape != shape:
+        _want(t, _bf16, name, 3)
         if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        _refuse(t, torch.bfloat16, 3, dev, name)
+        _refuse(t, _bf16, 3, dev, name)
     n, h, d = shape
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and h != 1):
@@ -191,7 +200,7 @@ def _rows_arg(t, shape, dev: int, name: str) -> tuple[int, int]:
 
 
 def _pool_arg(pool, dev: int) -> PkvPool:
-    base = _arg(pool, torch.bfloat16, 6, dev, "pool")
+    base = _arg(pool, _bf16, 6, dev, "pool")
     two, L, NP, P, H, D = pool.shape
     if two != 2:
         raise ValueError("pool dim 0 must be 2 (K, V)")
@@ -201,13 +210,13 @@ def _pool_arg(pool, dev: int) -> PkvPool:
 def _queries(q, o, lse, dev: int):
     """Addresses of q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None)."""
     shape = q.shape
-    qp = _arg(q, torch.bfloat16, 3, dev, "q")
-    op = _arg(o, torch.bfloat16, 3, dev, "o")
+    qp = _arg(q, _bf16, 3, dev, "q")
+    op = _arg(o, _bf16, 3, dev, "o")
     if o.shape != shape:
         raise ValueError("o must match q")
     if lse is None:
         return qp, op, None
-    lp = _arg(lse, torch.float32, 2, dev, "lse")
+    lp = _arg(lse, _f32, 2, dev, "lse")
     if lse.shape != shape[:2]:
         raise ValueError("lse must be [T, Hq]")
     return qp, op, lp
@@ -216,16 +225,16 @@ def _queries(q, o, lse, dev: int):
 def _tables(page_table, seq_lens, table_idx, batch: int, dev: int):
     """Addresses of page_table [rows, stride], seq_lens [B], table_idx [B] (or None), and the
     table's stride."""
-    pp = _arg(page_table, torch.int32, 2, dev, "page_table")
+    pp = _arg(page_table, _i32, 2, dev, "page_table")
     rows, stride = page_table.shape
-    sp = _arg(seq_lens, torch.int32, 1, dev, "seq_lens")
+    sp = _arg(seq_lens, _i32, 1, dev, "seq_lens")
     if seq_lens.shape[0] != batch:
         raise ValueError("seq_lens must have batch entries")
     if table_idx is None:
         if rows < batch:
             raise ValueError("page_table must have a row per request")
         return pp, sp, None, stride
-    tp = _arg(table_idx, torch.int32, 1, dev, "table_idx")
+    tp = _arg(table_idx, _i32, 1, dev, "table_idx")
     if table_idx.shape[0] != batch:
         raise ValueError("table_idx must have batch entries")
     return pp, sp, tp, stride
@@ -233,7 +242,7 @@ def _tables(page_table, seq_lens, table_idx, batch: int, dev: int):
 
 def _ints(t, n: int, dev: int, name: str) -> int:
     """Address of an int32 tensor of n entries."""
-    p = _arg(t, torch.int32, 1, dev, name)
+    p = _arg(t, _i32, 1, dev, name)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries")
     return p
@@ -287,7 +296,7 @@ def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc,
     append k and v to the pool at out_loc [N]; rows may be strided (slices of a fused projection).
     cos_sin [positions, rot_dim] fp32, cosines first, or None (no rotation: positions may be None);
     q_norm, k_norm [D] bf16 weights or None. q and q_out None: append only."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     ps = _pool_arg(pool, dev)
     n, d = k.shape[0], ps.head_dim
     kv_shape = (n, ps.num_kv_heads, d)
@@ -300,24 +309,24 @@ def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc,
     if q is not None:
         hq = q.shape[1]
         qp, qs = _rows_arg(q, (n, hq, d), dev, "q")
-        op = _arg(q_out, torch.bfloat16, 3, dev, "q_out")
+        op = _arg(q_out, _bf16, 3, dev, "q_out")
         if q_out.shape != q.shape:
             raise ValueError("q_out must match q")
     if cos_sin is not None:
-        tp = _arg(cos_sin, torch.float32, 2, dev, "cos_sin")
+        tp = _arg(cos_sin, _f32, 2, dev, "cos_sin")
         rows, rot = cos_sin.shape
         pp = _ints(positions, n, dev, "positions")
     if q_norm is not None:
-        qn = _arg(q_norm, torch.bfloat16, 1, dev, "q_norm")
+        qn = _arg(q_norm, _bf16, 1, dev, "q_norm")
         if q_norm.shape[0] != d:
             raise ValueError("q_norm must have head_dim entries")
     if k_norm is not None:
-        kn = _arg(k_norm, torch.bfloat16, 1, dev, "k_norm")
+        kn = _arg(k_norm, _bf16, 1, dev, "k_norm")
         if k_norm.shape[0] != d:
             raise ValueError("k_norm must have head_dim entries")
     _check(load().pkv_norm_rope_kv_store(
         ctypes.byref(ps), int(layer), qp, qs, op, hq, kp, vp, ks, qn, kn, float(eps), tp, rows, rot,
-        bool(interleaved), pp, _ints(out_loc, n, dev, "out_loc"), n, _stream(stream)))
+        bool(interleaved), pp, _ints(out_loc, n, dev, "out_loc"), n, _handle(stream, dev)))
 
 
 def pkv_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -363,7 +372,7 @@ def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,
                dev: int) -> PkvScoreMod:
     sp = pp = None
     if alibi_slopes is not None:
-        sp = _arg(alibi_slopes, torch.float32, 1, dev, "alibi_slopes")
+        sp = _arg(alibi_slopes, _f32, 1, dev, "alibi_slopes")
         if alibi_slopes.shape[0] != hq:
             raise ValueError("alibi_slopes must have one entry per q head")
     if prefix_lens is not None:
@@ -378,7 +387,7 @@ def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens,
     """Decode attention under score rules: a soft cap, alibi_slopes [Hq] fp32, a window, and
     prefix_lens [B] int32 first keys that stay visible. max_keys_hint: a bound on the keys a
     request sees (min(seq_len, window + prefix) with a window)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     ps = _pool_arg(pool, dev)
     qp, op, lp = _queries(q, o, lse, dev)
     B, Hq, D = q.shape
@@ -389,7 +398,7 @@ def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens,
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_decode_attn_mod(
         ctypes.byref(ps), int(layer), qp, op, lp, pp, stride, tp, sp, B, Hq, float(scale), ctypes.byref(mod),
-        int(max_keys_hint), ws, ws_bytes, _stream(stream)))
+        int(max_keys_hint), ws, ws_bytes, _handle(stream, dev)))
 
 
 def pkv_paged_decode_attn_store(pool, layer: int, q, k_new, v_new, o, lse, page_table, seq_lens,
@@ -513,7 +522,7 @@ def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table
     """Extend attention under score rules (as pkv_paged_decode_attn_mod's), chunk query j of
     request r at position seq_lens[r] - c_r + j; prefix_lens also lets the queries inside the
     prefix see the keys behind them."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     ps = _pool_arg(pool, dev)
     qp, op, lp = _queries(q, o, lse, dev)
     T, Hq, D = q.shape
@@ -526,7 +535,7 @@ def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table
     _check(load().pkv_paged_extend_attn_mod(
         ctypes.byref(ps), int(layer), qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"), op, lp, pp, stride,
         tp, sp, B, T, Hq, float(scale), ctypes.byref(mod), int(max_seq_len_hint), int(max_total_keys_hint), ws,
-        ws_bytes, _stream(stream)))
+        ws_bytes, _handle(stream, dev)))
 
 
 def pkv_paged_extend_attn_store(pool, layer: int, q, k_new, v_new, qo_indptr, o, lse,
@@ -583,7 +592,7 @@ def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_ta
     """Attention of drafted tokens: q, o [T, Hq, D] bf16, qo_indptr [B+1] and parents [T] int32
     (index within the request, -1 for a root); lse [T, Hq] fp32 or None; seq_lens count the
     drafted tokens, whose keys are in the pool."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     ps = _pool_arg(pool, dev)
     qp, op, lp = _queries(q, o, lse, dev)
     T, Hq, D = q.shape
@@ -595,7 +604,7 @@ def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_ta
     _check(load().pkv_paged_tree_attn(
         ctypes.byref(ps), int(layer), qp, _ints(qo_indptr, B + 1, dev, "qo_indptr"),
         _ints(parents, T, dev, "parents"), op, lp, pp, stride, tp, sp, B, T, Hq, float(scale),
-        int(max_tree_tokens), int(max_seq_len_hint), ws, ws_bytes, _stream(stream)))
+        int(max_tree_tokens), int(max_seq_len_hint), ws, ws_bytes, _handle(stream, dev)))
 
 
 def pkv_cascade_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
