@@ -224,7 +224,9 @@ pkv_status pkv_paged_decode_attn_store(const pkv_pool *pool, int32_t layer, cons
  *   t - i < window)
  * so prefix_lens is a bidirectional prompt prefix (its queries see keys behind
  * them) and, beside a window, the first keys that stay visible. All zero: the
- * plain causal rule.
+ * plain causal rule. In extend, as without rules, a key that only some of a
+ * request's queries see has weight zero for the others, so a value row that is
+ * not finite reaches them too.
  */
 typedef struct {
   float soft_cap;              /* 0: none; else > 0, |scale| / soft_cap <= 1e6 */
@@ -399,8 +401,8 @@ pkv_status pkv_paged_extend_attn_mod(const pkv_pool *pool, int32_t layer, const 
 /*
  * Bytes of device workspace pkv_paged_tree_attn needs for these host-side
  * sizes on the current device: fp32 states of the requests whose keys are
- * shared by several CTAs (0 where nothing can be; about 40 MB at most, plus
- * 8 bytes per request). 0 for invalid sizes. max_tree_tokens: a bound on the
+ * shared by several CTAs (0 where nothing can be; about 40 MB at most, plus 16
+ * bytes per 128 or 256 query rows of a request). 0 for invalid sizes. max_tree_tokens: a bound on the
  * drafted tokens of a request, 1 .. PKV_MAX_TREE_TOKENS; max_seq_len_hint: a
  * bound on every seq_len (>= 1).
  */
@@ -432,8 +434,10 @@ size_t pkv_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_k
  * pair or more drafted tokens than keys (PKV_DEVERR_INDPTR), a seq_len outside
  * the row (PKV_DEVERR_SEQ_LEN_RANGE), a negative table_idx. A parent that is
  * not -1 or an earlier token counts as -1 (PKV_DEVERR_TREE). A key on a bad
- * page reads as zeros (PKV_DEVERR_PAGE_RANGE). Rows of o and lse that belong
- * to no request are left as they were. K/V rows of pages of 8 and more tokens
+ * page reads as zeros (PKV_DEVERR_PAGE_RANGE). A drafted key that a token does
+ * not see has weight zero for it, so a value row that is not finite reaches the
+ * request's other drafts too. Rows of o and lse that belong to no request are
+ * left as they were. K/V rows of pages of 8 and more tokens
  * (a multiple of 8) are read by TMA, others by 16-byte copies.
  */
 pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *q,

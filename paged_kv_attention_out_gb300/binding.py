@@ -162,12 +162,14 @@ def _contig(t: torch.Tensor, name: str):
 # The calls below are launch-bound at decode sizes, so each tensor is checked by
 # one short expression; what is wrong is found out only when something is.
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
-_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its lazy set-up
-_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device() -> int:
+    return torch._C._cuda_getDevice()  # torch.cuda.current_device without its lazy set-up
 
 
 def _handle(stream, dev: int) -> int:
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _refuse(t, dtype, ndim: int, dev: int, name: str):
@@ -377,6 +379,8 @@ def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,
             raise ValueError("alibi_slopes must have one entry per q head")
     if prefix_lens is not None:
         pp = _ints(prefix_lens, batch, dev, "prefix_lens")
+    if window > 0x7fffffff:
+        raise ValueError("window must fit 32 bits")
     return PkvScoreMod(float(soft_cap), sp, int(window), pp)
 
 

@@ -326,11 +326,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
-// Score rules in the softmax. A tile is near if a bound of each row's scores
-// comes with the loads (the largest absolute raw score of each 32 columns
-// under a cap, the largest raw one under a bias alone), every raw score is in
-// the short polynomial's range, no column is masked and the bias is not so
-// steep that the bound would be far off (see extend.cu).
 template <int D, int kQT, bool kTma, int kRules>
 __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32, 1)
     direct_kernel(const __grid_constant__ CUtensorMap k_map,
@@ -850,8 +845,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
     for (;;) {
       // The segment, looked at here for what the tile loop needs and loaded
       // again after it (a cache hit), so that a thread holding a whole score
-      // row holds little else: rules with the segment live across the loop
-      // spilled 440 bytes and took 2.4 us per pair of tiles, against 1.5.
+      // row holds little else across the loop.
       Walk ahead_of = walk;
       if (!next_segment<kQT, kRules>(a, blocks, ahead_of, sg)) break;
       const bool shared = kQT == 2 && shared_tile(a, sg);

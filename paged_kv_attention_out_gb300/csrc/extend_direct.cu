@@ -15,9 +15,9 @@ namespace pkv {
 // are fewer (block, kv head) pairs N than SMs, the direct one shares N T tiles
 // out evenly, at more per tile and with a merge. (D = 128, page size 16, cap 50
 // and window 4096, direct / gathered: 4 requests of one token over up to 2000
-// keys 25 / 34; 2 of 64 over up to 8000 keys 37 / 65; 2 of up to 300 over up to
-// 1500 keys 36 / 32; 1 of 1000 over 3000 keys 62 / 49; 4 of up to 2048 over up
-// to 8192 keys 258 / 190.)
+// keys 23 / 34; 2 of 64 over up to 8000 keys 36 / 65; 2 of up to 300 over up to
+// 1500 keys 35 / 32; 1 of 1000 over 3000 keys 61 / 49; 4 of up to 2048 over up
+// to 8192 keys 251 / 190.)
 static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
   const double gathered = 12.0 + 1.5 * tiles * ((pairs + sms - 1) / sms);
   const double direct = 24.0 + 2.1 * static_cast<double>(pairs) * tiles / sms;

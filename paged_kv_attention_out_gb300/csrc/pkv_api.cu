@@ -308,9 +308,10 @@ static pkv_status score_rules(const pkv_score_mod *mod, float scale, pkv::ScoreR
         fmin(c == 0.0 ? 3e38 : pkv::kTanhNear / fabs(c), c1 == 0.0 ? 3e38 : pkv::kNearLog2 / fabs(c1)));
   }
   out->alibi_slopes = mod->alibi_slopes;
-  out->window = mod->window;
+  // a window longer than any row is none (and the kernels' distances stay in 32 bits)
+  out->window = mod->window >= 0x7fffff00 ? 0 : mod->window;
   out->prefix_lens = mod->prefix_lens;
-  *used = mod->soft_cap > 0.f || mod->alibi_slopes || mod->window > 0 || mod->prefix_lens;
+  *used = mod->soft_cap > 0.f || mod->alibi_slopes || out->window > 0 || mod->prefix_lens;
   return PKV_OK;
 }
 

@@ -404,6 +404,27 @@ def test_replay_in_a_graph_follows_new_lengths(kind):
     assert torch.isfinite(o.float()).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 257, 2 ** 30])
+@pytest.mark.parametrize("kind", ["decode", "extend", "few"])
+def test_a_window_longer_than_every_row(kind, window):
+    """Nothing is masked, and no distance leaves 32 bits: the causal answer."""
+    seq, chunks = [1, 700, 129, 400], [1, 300, 129, 200]
+    if kind == "few":  # the direct form
+        seq, chunks = [3900, 1], [40, 1]
+    case = W.random_case(9, kind="decode" if kind == "decode" else "extend", seq_lens=seq,
+                         chunk_lens=None if kind == "decode" else chunks, Hq=8, Hkv=2, D=64, P=16)
+    o, lse = mod_check(Rules(case, cap=20.0, window=window))
+    want, lse0 = mod_run(Rules(case, cap=20.0))
+    assert torch.equal(o, want) and torch.equal(lse, lse0)
+
+
+def test_a_window_past_32_bits_is_refused():
+    from paged_kv_attention_out_gb300 import binding
+    with pytest.raises(ValueError):
+        binding._score_mod(0.0, None, 2 ** 32 + 5, None, 1, 1, 0)
+
+
 def _decode(lib, pool, mod, hint=16):
     return lib.pkv_paged_decode_attn_mod(ctypes.byref(pool), 0, 1 << 20, 1 << 20, None, 64, 8, None,
                                          64, 1, 4, ctypes.c_float(0.125), ctypes.byref(mod), hint,
