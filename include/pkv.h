@@ -402,9 +402,9 @@ pkv_status pkv_paged_extend_attn_mod(const pkv_pool *pool, int32_t layer, const 
  * Bytes of device workspace pkv_paged_tree_attn needs for these host-side
  * sizes on the current device: fp32 states of the requests whose keys are
  * shared by several CTAs (0 where nothing can be; about 40 MB at most, plus 16
- * bytes per 128 or 256 query rows of a request). 0 for invalid sizes. max_tree_tokens: a bound on the
- * drafted tokens of a request, 1 .. PKV_MAX_TREE_TOKENS; max_seq_len_hint: a
- * bound on every seq_len (>= 1).
+ * bytes per 128 or 256 query rows of a request). 0 for invalid sizes.
+ * max_tree_tokens: a bound on the drafted tokens of a request, 1 ..
+ * PKV_MAX_TREE_TOKENS; max_seq_len_hint: a bound on every seq_len (>= 1).
  */
 size_t pkv_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                int32_t head_dim, int32_t max_tree_tokens,

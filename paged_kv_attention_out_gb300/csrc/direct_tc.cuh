@@ -169,8 +169,8 @@ struct DirectArgs {
   unsigned *err;
 };
 
-// Most requests, and blocks in all, of a call under rules: one thread each
-// finds a request's blocks, and a block's request.
+// Most requests, and blocks in all (max_blocks), of a call under rules: one
+// thread each finds a request's blocks, and a block's request.
 constexpr int kMaxRuleRequests = 256;
 constexpr int kMaxRuleBlocks = 352;
 
@@ -434,10 +434,12 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
         n = bad ? 0 : (end - beg + tpb - 1) / tpb;
       }
       const long long end = scan(n, round);
-      // (malformed tables could hold more blocks than the call has tokens for)
-      if (tid < a.batch)
-        s_first[tid] = static_cast<uint16_t>(min(end - n, static_cast<long long>(kMaxRuleBlocks)));
-      blocks.count = static_cast<int>(min(round, static_cast<long long>(kMaxRuleBlocks)));
+      // malformed tables can hold more blocks than the call has tokens for (and
+      // `table` entries): those past the bound, all of requests behind the
+      // first malformed pair, are left out
+      const long long most = a.max_blocks;
+      if (tid < a.batch) s_first[tid] = static_cast<uint16_t>(min(end - n, most));
+      blocks.count = static_cast<int>(min(round, most));
       __syncthreads();
     }
     const int nblocks = blocks.count;

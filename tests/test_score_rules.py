@@ -405,6 +405,30 @@ def test_replay_in_a_graph_follows_new_lengths(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [2500, 700])
+def test_malformed_tables_with_more_blocks_than_tokens(n):
+    """Pairs that overlap hold more query blocks than the call has tokens for: the rest is left out
+    and nothing is written behind the workspace (blocks that share groups, then one to a group)."""
+    import paged_kv_attention_out_gb300 as pkv
+    ensure_built()
+    case = W.random_case(17, kind="extend", seq_lens=[n] * 5, chunk_lens=[160] + [1] * 4, Hq=16,
+                         Hkv=1, D=64, P=16)
+    rules = Rules(case, cap=20.0)
+    pool, k, v, q, t = gpu_inputs(case)
+    pkv.pkv_kv_store(pool, case.layer, k, v, t["out_loc"])
+    pkv.pkv_read_device_errors()
+    o, lse = nan_outputs(q)
+    size = pkv.pkv_extend_mod_workspace_size(5, case.total_q, 16, 1, 64, n, 5 * n)
+    ws = torch.full((size + 65536,), 0x5a, dtype=torch.uint8, device="cuda")
+    bad = torch.tensor([0, 160, 0, 160, 0, 160], dtype=torch.int32, device="cuda")
+    pkv.pkv_paged_extend_attn_mod(pool, case.layer, q, bad, o, lse, t["page_table"], t["seq_lens"],
+                                  case.scale, n, ws[:size], max_total_keys_hint=5 * n,
+                                  **rules.kwargs())
+    assert pkv.pkv_read_device_errors() == 0x8  # malformed pairs
+    assert bool((ws[size:] == 0x5a).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 256, 2 ** 31 - 257, 2 ** 30])
 @pytest.mark.parametrize("kind", ["decode", "extend", "few"])
 def test_a_window_longer_than_every_row(kind, window):
