@@ -25,6 +25,9 @@
 // for one that goes on in the next) and a second kernel merges them; every
 // other block is written directly.
 //
+// A call with few, short blocks gives each its own group instead: no share to
+// find, no partial state, no second kernel.
+//
 // Roles of a CTA (kQT = 1 or 2 query tiles of 128 rows):
 //   warps 0 .. 4 kQT - 1  softmax: one query row per thread (TMEM lane)
 //   next warp             TMEM allocation and the MMAs. The warp stays together
@@ -156,6 +159,7 @@ struct DirectArgs {
   int32_t read_once;       // no K/V byte is read by more than one block
   int32_t max_blocks;  // entries of `table`
   int32_t groups;
+  int32_t whole;       // group i takes block i (groups = max_blocks), nothing is shared or merged
   TileCost cost;
   int32_t box;           // rows of a K/V TMA box (kTma)
   float scale_log2;      // |scale| log2(e) (log2(e) for scale 0), > 0
@@ -442,68 +446,77 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       blocks.count = static_cast<int>(min(round, most));
       __syncthreads();
     }
-    const int nblocks = blocks.count;
-    struct Cost {
-      int tiles, unit, extra, t_base, tokens;
-    };
-    auto cost_of = [&](int b, bool report, Cost &c) -> long long {
-      c = Cost{0, 1, 0, 0, 0};
-      if (b >= nblocks) return 0;
-      const Block k = load_block<kQT, kRules>(a, blocks, b, kRules == 0 && report);
-      if (k.tiles == 0) return 0;
-      c = Cost{k.tiles, k.cost, k.extra, k.t_base, k.tokens};
-      return k.extra + static_cast<long long>(k.tiles) * k.cost;
-    };
-    Cost unit0, unit;
-    const long long mine = cost_of(tid, lead, unit0);
-    const long long first_end = scan(mine, round);
-    const long long first_total = round;
-    total = round;
-    for (int b0 = kThreads; b0 < nblocks; b0 += kThreads) {
-      scan(cost_of(b0 + tid, lead, unit), round);
-      total += round;
-    }
-    // at least one tile begins in every share that a block covers
-    const int least = max(kMinTiles * a.cost.one, kBlockTiles * a.cost.one + a.cost.two);
-    const long long per = max(static_cast<long long>(least), div_up(total, a.groups));
-    const long long lo = per * blockIdx.y;
-    const long long hi = min(total, lo + per);
-    long long base = 0;
-    for (int b0 = 0; b0 < nblocks && (lead || base <= lo); b0 += kThreads) {
-      const int b = b0 + tid;
-      long long cost = mine;
-      unit = unit0;
-      if (b0 > 0) cost = cost_of(b, false, unit);
-      long long end = first_end;
-      round = first_total;
-      if (b0 > 0) end = scan(cost, round);
-      end += base;
-      const long long start = end - cost;
-      if (cost > 0 && start <= lo && lo < end && lo < hi) {
-        // the first tile that begins in the share
-        const long long first =
-            lo > start ? max(1ll, div_up(max(0ll, lo - start - unit.extra), unit.unit)) : 0;
-        const long long at = start + (first > 0 ? unit.extra : 0) + first * unit.unit;
-        s_walk = Walk{b, static_cast<int>(first), hi - at};
+    if (a.whole) {  // block i is all that group i has
+      const int b = static_cast<int>(blockIdx.y);
+      blocks.count = min(blocks.count, b + 1);
+      if (tid == 0) {
+        if (kRules == 0 && blockIdx.x == 0) load_block<kQT, kRules>(a, blocks, b, true);
+        s_walk = Walk{b, 0, 0x7fffffff};
       }
-      if (lead && b < nblocks && a.groups > 1) {
-        // which groups the block's tiles begin in (the merge reads this)
-        int4 e = make_int4(-1, -1, unit.t_base, unit.tokens);
-        if (cost > 0) {
-          const long long last = unit.tiles > 1 ? end - unit.unit : start;
-          const int g0 = static_cast<int>(div_down(start, per));
-          const int g1 = static_cast<int>(div_down(last, per));
-          if (g1 > g0) e.x = g0, e.y = g1;
+    } else {
+      const int nblocks = blocks.count;
+      struct Cost {
+        int tiles, unit, extra, t_base, tokens;
+      };
+      auto cost_of = [&](int b, bool report, Cost &c) -> long long {
+        c = Cost{0, 1, 0, 0, 0};
+        if (b >= nblocks) return 0;
+        const Block k = load_block<kQT, kRules>(a, blocks, b, kRules == 0 && report);
+        if (k.tiles == 0) return 0;
+        c = Cost{k.tiles, k.cost, k.extra, k.t_base, k.tokens};
+        return k.extra + static_cast<long long>(k.tiles) * k.cost;
+      };
+      Cost unit0, unit;
+      const long long mine = cost_of(tid, lead, unit0);
+      const long long first_end = scan(mine, round);
+      const long long first_total = round;
+      total = round;
+      for (int b0 = kThreads; b0 < nblocks; b0 += kThreads) {
+        scan(cost_of(b0 + tid, lead, unit), round);
+        total += round;
+      }
+      // at least one tile begins in every share that a block covers
+      const int least = max(kMinTiles * a.cost.one, kBlockTiles * a.cost.one + a.cost.two);
+      const long long per = max(static_cast<long long>(least), div_up(total, a.groups));
+      const long long lo = per * blockIdx.y;
+      const long long hi = min(total, lo + per);
+      long long base = 0;
+      for (int b0 = 0; b0 < nblocks && (lead || base <= lo); b0 += kThreads) {
+        const int b = b0 + tid;
+        long long cost = mine;
+        unit = unit0;
+        if (b0 > 0) cost = cost_of(b, false, unit);
+        long long end = first_end;
+        round = first_total;
+        if (b0 > 0) end = scan(cost, round);
+        end += base;
+        const long long start = end - cost;
+        if (cost > 0 && start <= lo && lo < end && lo < hi) {
+          // the first tile that begins in the share
+          const long long first =
+              lo > start ? max(1ll, div_up(max(0ll, lo - start - unit.extra), unit.unit)) : 0;
+          const long long at = start + (first > 0 ? unit.extra : 0) + first * unit.unit;
+          s_walk = Walk{b, static_cast<int>(first), hi - at};
         }
-        a.table[b] = e;
+        if (lead && b < nblocks && a.groups > 1) {
+          // which groups the block's tiles begin in (the merge reads this)
+          int4 e = make_int4(-1, -1, unit.t_base, unit.tokens);
+          if (cost > 0) {
+            const long long last = unit.tiles > 1 ? end - unit.unit : start;
+            const int g0 = static_cast<int>(div_down(start, per));
+            const int g1 = static_cast<int>(div_down(last, per));
+            if (g1 > g0) e.x = g0, e.y = g1;
+          }
+          a.table[b] = e;
+        }
+        base += round;
       }
-      base += round;
+      // entries of blocks that the call turned out not to have: the merge's grid
+      // is sized by a host bound, and the workspace holds anything on entry
+      if (lead && a.groups > 1)
+        for (int b = nblocks + tid; b < a.max_blocks; b += kThreads)
+          a.table[b] = make_int4(-1, -1, 0, 0);
     }
-    // entries of blocks that the call turned out not to have: the merge's grid
-    // is sized by a host bound, and the workspace holds anything on entry
-    if (lead && a.groups > 1)
-      for (int b = nblocks + tid; b < a.max_blocks; b += kThreads)
-        a.table[b] = make_int4(-1, -1, 0, 0);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -1132,12 +1145,16 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
       constexpr int kRows = kQT * kM;
       const int64_t part = static_cast<int64_t>(sg.slot) * a.hkv + kvh;
       float4 *po = reinterpret_cast<float4 *>(a.part_o) + part * (D / 4) * kRows + xq * kM + r;
+      // O's columns, all at once where the registers hold them: one round trip
+      constexpr int kO = kQT == 1 ? D : 32;
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        float o[32];
+      for (int cb = 0; cb < D / kO; ++cb) {
+        float o[kO];
         if (n_x > 0) {
-          tmem_ld32(orow_t + cb * 32, o);
-          if (shared) {
+#pragma unroll
+          for (int q = 0; q < kO / 32; ++q)
+            tmem_ld32(orow_t + cb * kO + q * 32, *reinterpret_cast<float(*)[32]>(&o[q * 32]));
+          if (kQT == 2 && shared) {
             float o1[32];
             tmem_ld32(orow_t + kN + cb * 32, o1);
             tmem_ld_wait();
@@ -1146,25 +1163,25 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
           } else {
             tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] *= f0;
+            for (int q = 0; q < kO; ++q) o[q] *= f0;
           }
         } else {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = 0.f;
+          for (int q = 0; q < kO; ++q) o[q] = 0.f;
         }
         if (valid) {
           if (sg.whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>(a.o + orow * D + cb * 32);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.o + orow * D + cb * kO);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < kO / 8; ++q)
               dst[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]),
                                   pack_bf16(o[8 * q + 2], o[8 * q + 3]),
                                   pack_bf16(o[8 * q + 4], o[8 * q + 5]),
                                   pack_bf16(o[8 * q + 6], o[8 * q + 7]));
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              po[(cb * 8 + q) * kRows] =
+            for (int q = 0; q < kO / 4; ++q)
+              po[(cb * (kO / 4) + q) * kRows] =
                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
@@ -1308,29 +1325,51 @@ cudaError_t launch(const DirectArgs &a, const CUtensorMap &km, const CUtensorMap
   const dim3 grid(a.hkv, a.groups), block((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32);
   e = launch_pdl(direct_kernel<D, kQT, kTma, kRules>, grid, block, S::kTotal, stream, km, vm, qm,
                  a);
-  if (e != cudaSuccess || a.groups == 1) return e;
+  if (e != cudaSuccess || a.groups == 1 || a.whole) return e;
   const dim3 mgrid(a.max_blocks, a.hkv, kQT * kM / kMergeRows);
   return launch_pdl(direct_merge_kernel<D, kQT>, mgrid, dim3(kMergeThreads), 0, stream, a);
 }
 
-// Groups of a call of at most `blocks` query blocks and max_seq keys, and the
-// workspace for their partial states and the block table (0 for one group).
+// In key tiles: what the search for a share, the partial states and the second
+// kernel cost a call (about 6 us), and what a further block in a share costs it.
+constexpr int share_cost(int query_tiles) { return query_tiles == 1 ? 8 : 6; }
+constexpr int kFurtherBlock = 8;
+
+// Groups of a call of at most `blocks` query blocks, each of at most
+// block_tiles key tiles, and max_seq keys, and the workspace for partial states
+// and the block table (0 if nothing can be shared; the same whether the call
+// shares or not, so that it grows with the sizes).
+//
+// A group for each block, or equal shares? The longest block's tiles against a
+// share's, about half of blocks * tiles / groups (lengths are ragged, the bound
+// is the longest). Per call, 32/8 heads of 128, page size 1, a group for each
+// block / shared: 1 request of 520 keys, 8 drafts 11.2 / 13.6 us, of 900 14.7 /
+// 16.2, of 1400 17.3 / 15.4; 16 of up to 2000 25.1 / 30.2, of 2900 31.4 / 31.6;
+// 64 drafts: 1 of 520 17.8 / 18.8, of 900 22.2 / 20.6; 16 of up to 2000 38.4 /
+// 39.2, of 2900 47.7 / 37.5.
 inline DirectPlan plan(int32_t blocks, int32_t query_tiles, int32_t hkv, int32_t d,
-                       int32_t max_seq, int32_t sm_count) {
+                       int32_t max_seq, int64_t block_tiles, int32_t sm_count) {
   DirectPlan p{};
   p.query_tiles = query_tiles;
+  p.max_blocks = blocks;
   // one group per Hkv SMs, and no more than there are smallest shares
+  const int64_t all = std::max<int64_t>(1, (sm_count > 0 ? sm_count : 1) / hkv);
   const int64_t tiles =
       static_cast<int64_t>(blocks) * ((static_cast<int64_t>(max_seq) + kN - 1) / kN);
-  int64_t groups = std::max<int64_t>(1, (sm_count > 0 ? sm_count : 1) / hkv);
-  groups = std::min<int64_t>(groups, std::max<int64_t>(1, (tiles + kMinTiles - 1) / kMinTiles));
+  const int64_t groups =
+      std::min<int64_t>(all, std::max<int64_t>(1, (tiles + kMinTiles - 1) / kMinTiles));
   p.groups = static_cast<int32_t>(groups);
-  p.max_blocks = blocks;
   if (groups > 1) {
     const size_t rows = static_cast<size_t>(2 * groups) * hkv * query_tiles * kM;
     p.lse_offset = rows * d * sizeof(float);
     p.table_offset = (p.lse_offset + rows * sizeof(float) + 255) & ~size_t(255);
     p.workspace_bytes = p.table_offset + sizeof(int4) * static_cast<size_t>(blocks);
+  }
+  if (blocks <= all &&
+      2 * all * (block_tiles - share_cost(query_tiles)) <=
+          blocks * (block_tiles + kFurtherBlock)) {
+    p.whole = 1;
+    p.groups = blocks;
   }
   return p;
 }
@@ -1363,6 +1402,7 @@ inline bool direct_args(DirectArgs *out, CUtensorMap *km, CUtensorMap *vm, CUten
   a.tokens_per_tile = kM / a.group;
   a.max_blocks = plan.max_blocks;
   a.groups = plan.groups;
+  a.whole = plan.whole;
   a.cost = tile_cost(g.d);
   a.q_mode = scale > 0.f ? 0 : (scale < 0.f ? 1 : 2);
   a.scale_log2 = scale > 0.f ? scale * kLog2e : (scale < 0.f ? -scale * kLog2e : kLog2e);

@@ -24,6 +24,12 @@ static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
   return direct < gathered;
 }
 
+// A call whose blocks have a group each and no more key tiles than this takes
+// the direct form for its one launch (16/8 heads of 64, distance bias: 2 of 48
+// over up to 200 keys 9.4 us against 11.1 gathered, 400 keys 12.1 / 13.6, 800
+// 15.4 / 17.2; 32/8 of 128: 13.3 / 14.0, 18.6 / 16.8, 23.5 / 22.6).
+constexpr int kOneLaunchTiles = 3;
+
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
                         int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan) {
   const int32_t tpb = 2 * (direct::kM / (hq / hkv));
@@ -34,9 +40,9 @@ bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv,
   if (window > 0)
     tiles = std::min<int64_t>(tiles, (static_cast<int64_t>(window) + tpb) / direct::kN + 2);
   const int64_t busy = std::max<int64_t>(batch, (static_cast<int64_t>(total_q) + tpb - 1) / tpb);
-  if (!direct_is_faster(busy * hkv, tiles, sm_count > 0 ? sm_count : 1)) return false;
-  *plan = direct::plan(static_cast<int32_t>(blocks), 2, hkv, d, max_seq, sm_count);
-  return true;
+  *plan = direct::plan(static_cast<int32_t>(blocks), 2, hkv, d, max_seq, tiles, sm_count);
+  return (plan->whole && tiles <= kOneLaunchTiles) ||
+         direct_is_faster(busy * hkv, tiles, sm_count > 0 ? sm_count : 1);
 }
 
 cudaError_t launch_extend_direct(const PoolGeom &g, int32_t layer, const void *q,

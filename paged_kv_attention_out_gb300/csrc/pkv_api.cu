@@ -614,7 +614,8 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
     if (pkv::extend_direct_plan(batch, total_q, num_q_heads, g.hkv, g.d,
                                 static_cast<int32_t>(cap),
                                 rules.prefix_lens ? 0 : rules.window, d->sm_count, &plan)) {
-      if ((s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)
+      if (!plan.whole &&
+          (s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)
         return s;
       const cudaError_t e = pkv::launch_extend_direct(
           g, layer, q, qo_indptr, o, lse, page_table, table_stride, table_idx, seq_lens, batch,

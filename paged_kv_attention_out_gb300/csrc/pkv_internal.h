@@ -158,6 +158,7 @@ struct DirectPlan {
   int32_t query_tiles;
   int32_t max_blocks;
   int32_t groups;
+  int32_t whole;  // a group per block, nothing shared
   size_t lse_offset;
   size_t table_offset;
   size_t workspace_bytes;
