@@ -54,18 +54,20 @@ CSRC = os.path.join(ROOT, "paged_kv_attention_out_gb300", "csrc")
 # it only while those sources are unchanged (else null).
 MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
-    "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'pkv_common.cuh'],
-               "sha256": "1946f3ac4ab631093fbc25b82b65651fec5fd69a755e14f8055eb573eab8ac9f",
-               "bytes": 625499392},
+    "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
+               "sha256": "b84cf1938260e9ec589fab4bbf76bd78b6b2db9e03c21b264ecfcdfe4f363fbd",
+               "bytes": 623414496},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
-    "extend": {"sources": ['extend.cu', 'tc_common.cuh', 'pkv_common.cuh'],
-               "sha256": "603ff433c0bcf92b10475c79a715087cc51e548d1834ee93f00ce253edbfd45c",
-               "bytes": 489539904},
+    "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
+                           'pkv_common.cuh'],
+               "sha256": "c6b573a0e35b59a562fafa66fbe4c299883b60b354df599b95cacc883e303d6c",
+               "bytes": 493066560},
     # cascade_prefix_kernel + decode_kernel (suffix) + decode_merge_narrow_kernel,
     # radix-shared decode through cascade decode
-    "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'tc_common.cuh', 'pkv_common.cuh'],
-                "sha256": "3e5d0f458ab7b66880974acc5521cb2eb68108f6736d1a82d0963b3ff761b592",
-                "bytes": 372296352},
+    "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
+                            'tc_common.cuh', 'pkv_common.cuh'],
+                "sha256": "ecf14c79d6bc6bba35d680eb3bb1a020bb94fc9678a3a1f1215cb636059531fd",
+                "bytes": 372320981},
 }
 
 

@@ -163,6 +163,84 @@ __device__ __forceinline__ void merge_pair(const Args &a, int64_t bh, int lane) 
   if (lane == 0 && a.lse) a.lse[bh] = L > 0.f ? ref + logf(L) : -INFINITY;
 }
 
+// The same merge for many states of few (request, q head) pairs (calls with
+// score rules): a CTA of eight warps per pair, each warp with every eighth
+// state and a running maximum, joined in shared memory. One round trip to L2
+// for up to 64 states, where a lone warp makes one for each eight after the
+// first sixteen: rows up to 32000 keys, whole call, wide / a warp per pair: 1
+// row of 28/4 heads of 64 16.5 / 43.4 us, of 32/8 of 128 41.8 / 64.2, 8 rows of
+// 16/16 148 / 153, 32 of 32/8 (1024 pairs) 284.8 / 285.3, 64 (2048) 560 / 554:
+// wide while its CTAs are one wave.
+constexpr int kWideWarps = 8;
+constexpr int kWidePairsPerSm = 8;
+constexpr int kWideBatch = 8;
+
+template <int D, typename Args>
+__global__ void __launch_bounds__(kWideWarps * 32) decode_merge_wide_kernel(const Args a) {
+  constexpr int kCols = D / 32;  // per lane
+  __shared__ float s_o[kWideWarps][D];
+  __shared__ float2 s_ml[kWideWarps];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int64_t bh = blockIdx.x;
+  const int n = row_info(a, static_cast<int>(bh / a.hq), false).nsplit;
+  grid_dependency_wait();  // the partial states come from decode_kernel
+  if (n <= 1) return;      // written by it already
+  const float *pl = a.part_lse + bh * a.pstride;
+  const float *po = a.part_o + bh * a.pstride * D + lane * kCols;
+  float m = -INFINITY, l = 0.f;
+  float o[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+  for (int s0 = warp; s0 < n; s0 += kWideWarps * kWideBatch) {
+    float lse[kWideBatch], v[kWideBatch][kCols];
+#pragma unroll
+    for (int u = 0; u < kWideBatch; ++u) {
+      const int s = s0 + u * kWideWarps;
+      lse[u] = s < n ? pl[s] : -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[u][c] = s < n ? po[static_cast<int64_t>(s) * D + c] : 0.f;
+    }
+    float mx = m;
+#pragma unroll
+    for (int u = 0; u < kWideBatch; ++u) mx = fmaxf(mx, lse[u]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float f = expf(m - ref);
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] *= f;
+#pragma unroll
+    for (int u = 0; u < kWideBatch; ++u) {
+      const float w = expf(lse[u] - ref);
+      l += w;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[c] += w * v[u][c];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) s_o[warp][lane * kCols + c] = o[c];
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+  __syncthreads();
+  const int t = static_cast<int>(threadIdx.x);
+  if (t >= D / 2) return;  // two columns a thread
+  float M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWideWarps; ++w) M = fmaxf(M, s_ml[w].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWideWarps; ++w) {
+    const float f = expf(s_ml[w].x - ref);
+    L += f * s_ml[w].y;
+    x += f * s_o[w][2 * t];
+    y += f * s_o[w][2 * t + 1];
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<uint32_t *>(a.o + bh * D + 2 * t) = pack_bf16(x * inv, y * inv);
+  if (t == 0 && a.lse) a.lse[bh] = L > 0.f ? ref + logf(L) : -INFINITY;
+}
+
 // The same merge for plans with at most kNarrowStates states per (request,
 // q head) (suffix splits plus cascade prefix slots): a group of D / 16 lanes
 // per pair, 16 columns per lane, 32 / (D / 16) pairs per warp. A quarter of
@@ -263,9 +341,9 @@ DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d
 // Calls with score rules: half as long splits as plain decode. Rows are ragged
 // (a hint bounds the longest), so the CTAs of the average batch are half the
 // planned ones, and with eight planned per SM the last wave of three resident
-// ones is mostly empty: 8 rows up to 32768 keys of 16 kv heads 183 us at 8, 164
-// at 16, 174 at 32; 64 rows up to 16384 of 8 kv heads 323, 286, 270; with a
-// window of 4096 155, 155, 164.
+// ones is mostly empty: 8 rows up to 32768 keys of 16 kv heads 182 us at 8, 159
+// at 16, 163 at 32; 16 rows up to 8000 of 4 kv heads 18.5, 18.4, 18.5; 64 rows
+// up to 16384 of 8 kv heads with a window of 4096 155, 155, 164.
 #ifndef PKV_RULES_UNITS_PER_SM
 #define PKV_RULES_UNITS_PER_SM 16
 #endif
@@ -399,7 +477,17 @@ static cudaError_t launch_decode_rules(const DecodeArgs &base, const ScoreRules 
   else
     e = launch_decode_main(DecodeRulesArgs<0>(a), g, plan, batch, stream);
   if (e != cudaSuccess || plan.splits <= 1) return e;
-  return launch_decode_merge(DecodeRulesArgs<0>(a), g, batch, plan.sm_count, stream);
+  const DecodeRulesArgs<0> m(a);
+  const int64_t pairs = static_cast<int64_t>(batch) * a.hq;
+  if (plan.splits > kMergeBatch && pairs <= kWidePairsPerSm * static_cast<int64_t>(plan.sm_count)) {
+    const dim3 grid(static_cast<unsigned>(pairs)), block(kWideWarps * 32);
+    return g.d == 128
+               ? launch_pdl(decode_merge_wide_kernel<128, DecodeRulesArgs<0>>, grid, block, 0,
+                            stream, m)
+               : launch_pdl(decode_merge_wide_kernel<64, DecodeRulesArgs<0>>, grid, block, 0,
+                            stream, m);
+  }
+  return launch_decode_merge(m, g, batch, plan.sm_count, stream);
 }
 
 cudaError_t launch_decode(const PoolGeom &g, int32_t layer, const void *q, void *o, float *lse,

@@ -345,6 +345,19 @@ def test_decode_hint_changes_only_the_splits(hint):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rule", [dict(alibi=True), dict(cap=3.0, window=9000, prefix=[40, 0])],
+                         ids=str)
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 7, 1), (128, 4, 4), (128, 8, 1)])
+def test_decode_of_long_rows_merges_many_states(D, Hq, Hkv, rule):
+    """Over a hundred splits of one row, a few or one of the others; with and without lse."""
+    case = W.random_case(18, seq_lens=[20011, 1, 129, 2500], Hq=Hq, Hkv=Hkv, D=D, P=16)
+    rules = Rules(case, **rule)
+    o, _ = mod_check(rules)
+    same, _ = mod_run(rules, lse=False)
+    assert torch.equal(o, same)
+
+
+@pytest.mark.gpu
 def test_a_chunked_prompt_equals_the_whole():
     """A prefix-LM prompt in one chunk, and its causal rest in two: the second chunk sees the
     prefix that the first one stored."""
