@@ -243,7 +243,8 @@ typedef struct {
  * max_keys_hint: a bound on the keys a request sees, min(seq_len, window +
  * prefix) with a window; it sets the split plan as max_seq_len_hint does, and
  * the workspace is pkv_decode_mod_workspace_size(batch, Hq, Hkv, D,
- * max_keys_hint) bytes. A key on a bad page reads as zeros
+ * max_keys_hint) bytes (a workspace for a larger batch and hint serves a
+ * smaller one). A key on a bad page reads as zeros
  * (PKV_DEVERR_PAGE_RANGE).
  */
 size_t pkv_decode_mod_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -377,7 +378,8 @@ pkv_status pkv_paged_extend_attn_store(const pkv_pool *pool, int32_t layer, cons
  * Keys that no query of the request's chunk sees are not read, nor are their
  * page_table entries. Hints and refusals as for pkv_paged_extend_attn; the
  * workspace is pkv_extend_mod_workspace_size(batch, total_q, Hq, Hkv, D,
- * max_seq_len_hint, max_total_keys_hint) bytes. A call whose queries are few
+ * max_seq_len_hint, max_total_keys_hint) bytes (one for larger sizes serves
+ * smaller ones). A call whose queries are few
  * for the keys they see reads K/V straight from the pool (a choice by these
  * host-side sizes); there a request past max_total_keys_hint is computed all
  * the same.

@@ -29,6 +29,8 @@
 //    seq_len, SM count), so the call never syncs and is graph-capturable.
 #include <math.h>
 
+#include <algorithm>
+
 #include "decode_common.cuh"
 #include "pkv_internal.h"
 
@@ -322,7 +324,9 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_narrow_kernel(cons
 }  // namespace
 
 static DecodePlan plan_splits(int32_t batch, int32_t hq, int32_t hkv, int32_t d,
-                              int32_t max_seq_len, int32_t sm_count, int32_t units_per_sm);
+                              int32_t max_seq_len, int32_t sm_count, int32_t units_per_sm,
+                              int32_t heads_per_cta = kDecodeWarps,
+                              int32_t min_tiles = PKV_DECODE_MIN_SPLIT_TILES);
 
 DecodePlan plan_decode(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_seq_len,
                        int32_t sm_count) {
@@ -338,38 +342,69 @@ DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d
   return plan_splits(batch, hq, hkv, d, max_seq_len, sm_count, PKV_CASCADE_UNITS_PER_SM);
 }
 
-// Calls with score rules: half as long splits as plain decode. Rows are ragged
-// (a hint bounds the longest), so the CTAs of the average batch are half the
-// planned ones, and with eight planned per SM the last wave of three resident
-// ones is mostly empty: 8 rows up to 32768 keys of 16 kv heads 182 us at 8, 159
-// at 16, 163 at 32; 16 rows up to 8000 of 4 kv heads 18.5, 18.4, 18.5; 64 rows
-// up to 16384 of 8 kv heads with a window of 4096 155, 155, 164.
+// Calls with score rules: a kv head's four warps to a CTA, where plain decode
+// has four kv heads' (a row's keys are then walked by four warps at a time: 1
+// row of 600 keys of 8 kv heads of 128 6.5 us instead of 11.6, 64 rows up to
+// 16384 with a window of 4096 148 instead of 153; 8 rows up to 32768 of 16 kv
+// heads 159 instead of 157).
+// Splits: 8 tiles while that makes no more CTAs than are resident at once (three
+// an SM), 16 and more beyond (1 row of 2000 keys 6.4 us with 8, 7.9 with 16; of
+// 8000 14.3, 11.1; 16 of up to 2000 21.9, 20.1), and planned for UNITS_PER_SM
+// CTAs an SM: rows are ragged, a hint bounds the longest.
 #ifndef PKV_RULES_UNITS_PER_SM
 #define PKV_RULES_UNITS_PER_SM 16
 #endif
 
 DecodePlan plan_decode_rules(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
                              int32_t sm_count) {
-  return plan_splits(batch, hq, hkv, d, max_keys, sm_count, PKV_RULES_UNITS_PER_SM);
+  constexpr int32_t kShort = PKV_DECODE_MIN_SPLIT_TILES;
+  const int64_t splits = (static_cast<int64_t>(max_keys) + kShort * kDecodeTileKeys - 1) /
+                         (kShort * kDecodeTileKeys);
+  const bool one_wave = batch * splits * hkv <= 3 * static_cast<int64_t>(sm_count);
+  DecodePlan p = plan_splits(batch, hq, hkv, d, max_keys, sm_count, PKV_RULES_UNITS_PER_SM, 1,
+                             one_wave ? kShort : 2 * kShort);
+  if (p.splits > 1)
+    p.workspace_bytes = decode_rules_workspace(batch, hq, hkv, d, max_keys, sm_count);
+  return p;
+}
+
+// States of the plan above, or of plain decode's, for any batch and hint up to
+// these: splits of the shortest length, or as many as are planned for the SMs
+// (UNITS_PER_SM CTAs with four kv heads each) and one more per row and head.
+size_t decode_rules_workspace(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
+                              int32_t sm_count) {
+  constexpr int64_t kShort = PKV_DECODE_MIN_SPLIT_TILES * kDecodeTileKeys;
+  static_assert(PKV_RULES_UNITS_PER_SM <= PKV_DECODE_UNITS_PER_SM * kDecodeWarps &&
+                    3 <= PKV_RULES_UNITS_PER_SM,
+                "the larger of the two plans");
+  const int64_t splits = (static_cast<int64_t>(max_keys) + kShort - 1) / kShort;
+  if (splits <= 1) return 0;
+  const int64_t pairs = static_cast<int64_t>(batch) * hq;
+  const int64_t planned = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) *
+                          PKV_DECODE_UNITS_PER_SM * kDecodeWarps * (hq / hkv);
+  const size_t rows = static_cast<size_t>(std::min(pairs * splits, planned + pairs));
+  const size_t o_bytes = (rows * d * sizeof(float) + 255) & ~size_t(255);
+  return o_bytes + ((rows * sizeof(float) + 255) & ~size_t(255));
 }
 
 static DecodePlan plan_splits(int32_t batch, int32_t hq, int32_t hkv, int32_t d,
-                              int32_t max_seq_len, int32_t sm_count, int32_t units_per_sm) {
+                              int32_t max_seq_len, int32_t sm_count, int32_t units_per_sm,
+                              int32_t heads_per_cta, int32_t min_tiles) {
   (void)hq;
   DecodePlan p{};
   p.sm_count = sm_count;
-  p.heads_per_cta = hkv >= kDecodeWarps ? kDecodeWarps : hkv;
+  p.heads_per_cta = hkv >= heads_per_cta ? heads_per_cta : hkv;
   p.warps_per_head = kDecodeWarps / p.heads_per_cta;
   p.head_groups = hkv / p.heads_per_cta;
   const int64_t max_seq = max_seq_len < 1 ? 1 : max_seq_len;
   const int64_t tiles = (max_seq + kDecodeTileKeys - 1) / kDecodeTileKeys;
   // Aim for about PKV_DECODE_UNITS_PER_SM CTAs of work per SM if every
-  // request were max_seq long, with at least PKV_DECODE_MIN_SPLIT_TILES tiles
+  // request were max_seq long, with at least min_tiles tiles
   // per split so partial states stay a few percent of the KV bytes.
   const int64_t units = static_cast<int64_t>(batch) * p.head_groups * tiles;
   const int64_t target = static_cast<int64_t>(sm_count > 0 ? sm_count : 1) * units_per_sm;
   int64_t chunk_tiles = (units + target - 1) / target;
-  if (chunk_tiles < PKV_DECODE_MIN_SPLIT_TILES) chunk_tiles = PKV_DECODE_MIN_SPLIT_TILES;
+  if (chunk_tiles < min_tiles) chunk_tiles = min_tiles;
   int64_t splits = (tiles + chunk_tiles - 1) / chunk_tiles;
   while (splits > 65535) {
     chunk_tiles *= 2;

@@ -30,10 +30,22 @@ static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
 // 15.4 / 17.2; 32/8 of 128: 13.3 / 14.0, 18.6 / 16.8, 23.5 / 22.6).
 constexpr int kOneLaunchTiles = 3;
 
+static int64_t block_bound(int32_t batch, int32_t total_q, int32_t tpb) {
+  return (static_cast<int64_t>(total_q) + tpb - 1) / tpb + batch;
+}
+
+size_t extend_direct_workspace(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
+                               int32_t max_seq, int32_t sm_count) {
+  const int64_t blocks = block_bound(batch, total_q, 2 * (direct::kM / (hq / hkv)));
+  return direct::plan(static_cast<int32_t>(std::min<int64_t>(blocks, direct::kMaxRuleBlocks)), 2,
+                      hkv, d, max_seq, 0, sm_count)
+      .workspace_bytes;
+}
+
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
                         int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan) {
   const int32_t tpb = 2 * (direct::kM / (hq / hkv));
-  const int64_t blocks = (static_cast<int64_t>(total_q) + tpb - 1) / tpb + batch;
+  const int64_t blocks = block_bound(batch, total_q, tpb);
   if (batch > direct::kMaxRuleRequests || blocks > direct::kMaxRuleBlocks) return false;
   // key tiles of a block: all up to the longest request's, or the window's
   int64_t tiles = (static_cast<int64_t>(max_seq) + direct::kN - 1) / direct::kN;

@@ -266,18 +266,14 @@ size_t pkv_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
 
 size_t pkv_decode_mod_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t head_dim, int32_t max_keys_hint) {
-  // (a call whose rules change nothing runs as plain decode, with its plan)
-  const size_t plain =
-      pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_keys_hint);
   if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       num_q_heads % num_kv_heads != 0)
     return 0;
   DevInfo *d = nullptr;
   if (device_info(&d) != PKV_OK) return 0;
-  const size_t ruled = pkv::plan_decode_rules(batch, num_q_heads, num_kv_heads, head_dim,
-                                              effective_hint(max_keys_hint), d->sm_count)
-                           .workspace_bytes;
-  return ruled > plain ? ruled : plain;
+  // (a call whose rules change nothing runs as plain decode, with its plan)
+  return pkv::decode_rules_workspace(batch, num_q_heads, num_kv_heads, head_dim,
+                                     effective_hint(max_keys_hint), d->sm_count);
 }
 
 // The score rules of a call as the kernels take them; *used = false if they
@@ -542,13 +538,10 @@ size_t pkv_extend_mod_workspace_size(int32_t batch, int32_t total_q, int32_t num
     return 0;
   DevInfo *d = nullptr;
   if (device_info(&d) != PKV_OK) return 0;
-  pkv::DirectPlan plan;
-  // (the size of the direct form for any window: it depends on the bound of
-  // the lengths alone)
-  if (!pkv::extend_direct_plan(batch, total_q, num_q_heads, num_kv_heads, head_dim,
-                               max_seq_len_hint, 0, d->sm_count, &plan))
-    return gathered;
-  return plan.workspace_bytes > gathered ? plan.workspace_bytes : gathered;
+  // either form may be the faster one for a smaller call
+  const size_t direct = pkv::extend_direct_workspace(
+      batch, total_q, num_q_heads, num_kv_heads, head_dim, max_seq_len_hint, d->sm_count);
+  return direct > gathered ? direct : gathered;
 }
 
 static pkv_status check_workspace(const void *workspace, size_t workspace_bytes, size_t need) {

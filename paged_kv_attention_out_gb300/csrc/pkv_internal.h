@@ -38,6 +38,8 @@ DecodePlan plan_decode(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_
 // The split plan of a decode with score rules.
 DecodePlan plan_decode_rules(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
                              int32_t sm_count);
+size_t decode_rules_workspace(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_keys,
+                              int32_t sm_count);
 // The split plan of a cascade's suffix decode (host scalars only).
 DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d,
                                int32_t max_seq_len, int32_t sm_count);
@@ -179,6 +181,9 @@ cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const i
 // requests than it takes, or the form of extend.cu is faster.
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
                         int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan);
+// Its workspace, for any window.
+size_t extend_direct_workspace(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
+                               int32_t max_seq, int32_t sm_count);
 cudaError_t launch_extend_direct(const PoolGeom &g, int32_t layer, const void *q,
                                  const int32_t *qo_indptr, void *o, float *lse,
                                  const int32_t *page_table, int64_t table_stride,

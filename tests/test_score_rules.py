@@ -500,3 +500,31 @@ def test_the_workspace_covers_both_plans_and_a_smaller_one_is_refused():
                                       case.scale, 5000, ws, soft_cap=5.0)
     assert e.value.status == 3
     assert pkv.pkv_decode_mod_workspace_size(0, 8, 2, 64, 5000) == 0
+
+
+@pytest.mark.gpu
+def test_a_workspace_for_larger_sizes_serves_smaller_ones():
+    import paged_kv_attention_out_gb300 as pkv
+    decode = lambda b, n, hq=8, hkv=2: pkv.pkv_decode_mod_workspace_size(b, hq, hkv, 64, n)
+    extend = lambda b, t, n, k: pkv.pkv_extend_mod_workspace_size(b, t, 8, 1, 64, n, k)
+    tree = lambda b, t, n: pkv.pkv_tree_workspace_size(b, 8, 2, 64, t, n)
+    grid = [1, 2, 3, 7, 16, 60, 200, 300]
+    keys = [1, 128, 129, 1000, 2000, 5000, 40000]
+    for a, b in zip(grid, grid[1:]):
+        for m, n in zip(keys, keys[1:]):
+            assert decode(a, m) <= decode(b, m) <= decode(b, n) and decode(a, m) <= decode(a, n)
+            assert decode(a, n) >= pkv.pkv_decode_workspace_size(a, 8, 2, 64, n)
+            assert extend(a, 2 * a, m, 100) <= extend(b, 2 * b, m, 100) <= extend(b, 2 * b, n, 5000)
+            assert tree(a, 5, m) <= tree(b, 5, m) <= tree(b, 70, n)
+    # a batch whose plan differs from that of the larger one, in its workspace
+    big = W.random_case(19, seq_lens=[2000] * 4, Hq=32, Hkv=8, D=64, P=16)
+    ws = torch.empty(pkv.pkv_decode_mod_workspace_size(4, 32, 8, 64, 2000), dtype=torch.uint8,
+                     device="cuda")
+    pool, k, v, q, t = gpu_inputs(big)
+    pkv.pkv_kv_store(pool, big.layer, k, v, t["out_loc"])
+    o, lse = nan_outputs(q)
+    want = Rules(big, window=1500).want()
+    for b in (1, 2, 3, 4):
+        pkv.pkv_paged_decode_attn_mod(pool, big.layer, q[:b], o[:b], lse[:b], t["page_table"][:b],
+                                      t["seq_lens"][:b], big.scale, 2000, ws, window=1500)
+        check(o[:b], lse[:b], tuple(x[:b] for x in want))
