@@ -350,7 +350,9 @@ DecodePlan plan_cascade_suffix(int32_t batch, int32_t hq, int32_t hkv, int32_t d
 // Splits: 8 tiles while that makes no more CTAs than are resident at once (three
 // an SM), 16 and more beyond (1 row of 2000 keys 6.4 us with 8, 7.9 with 16; of
 // 8000 14.3, 11.1; 16 of up to 2000 21.9, 20.1), and planned for UNITS_PER_SM
-// CTAs an SM: rows are ragged, a hint bounds the longest.
+// CTAs an SM: rows are ragged, a hint bounds the longest. Rows of up to 16 tiles
+// are not split: as long on the GPU (250 keys 6.0 us either way), and a launch
+// less for the host.
 #ifndef PKV_RULES_UNITS_PER_SM
 #define PKV_RULES_UNITS_PER_SM 16
 #endif
@@ -362,7 +364,7 @@ DecodePlan plan_decode_rules(int32_t batch, int32_t hq, int32_t hkv, int32_t d, 
                          (kShort * kDecodeTileKeys);
   const bool one_wave = batch * splits * hkv <= 3 * static_cast<int64_t>(sm_count);
   DecodePlan p = plan_splits(batch, hq, hkv, d, max_keys, sm_count, PKV_RULES_UNITS_PER_SM, 1,
-                             one_wave ? kShort : 2 * kShort);
+                             one_wave && splits > 2 ? kShort : 2 * kShort);
   if (p.splits > 1)
     p.workspace_bytes = decode_rules_workspace(batch, hq, hkv, d, max_keys, sm_count);
   return p;
