@@ -11,21 +11,24 @@
 namespace pkv {
 
 // Which of the two forms takes less time, in microseconds, by their measured
-// parts: the longest block (T key tiles) bounds the gathered form while there
-// are fewer (block, kv head) pairs N than SMs, the direct one shares N T tiles
-// out evenly, at more per tile and with a merge. (D = 128, page size 16, cap 50
-// and window 4096, direct / gathered: 4 requests of one token over up to 2000
-// keys 23 / 34; 2 of 64 over up to 8000 keys 36 / 65; 2 of up to 300 over up to
-// 1500 keys 35 / 32; 1 of 1000 over 3000 keys 61 / 49; 4 of up to 2048 over up
-// to 8192 keys 251 / 190.)
+// parts: the longest block (T key tiles, by the hint) bounds the gathered form
+// while there are fewer (block, kv head) pairs N than SMs, the direct one shares
+// the tiles out evenly, at more per tile and with a merge; a hint bounds the
+// longest row, the others are taken to be half as long and more. (Direct /
+// gathered, 32/8 heads of 128, page size 16, distance bias: 1 request of one
+// token over 800 keys 16.3 / 18.4, 4 over up to 800 21.2 / 18.1, over 1400 21.1 /
+// 26.2; 8 over up to 1400 23.8 / 28.6, up to 2000 24.7 / 35.9; 4 of up to 200
+// over up to 1400 33.7 / 31.1, up to 2900 42.1 / 54.3; 8 of up to 200 over up to
+// 1400 48.7 / 35.3. Cap 50 and window 4096: 1 of 1000 over 3000 keys 61 / 49; 4
+// of up to 2048 over up to 8192 251 / 190.)
 static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
   const double gathered = 12.0 + 1.5 * tiles * ((pairs + sms - 1) / sms);
-  const double direct = 24.0 + 2.1 * static_cast<double>(pairs) * tiles / sms;
+  const double direct = 21.5 + 1.5 * static_cast<double>(pairs) * tiles / sms;
   return direct < gathered;
 }
 
 // A call whose blocks have a group each and no more key tiles than this takes
-// the direct form for its one launch (16/8 heads of 64, distance bias: 2 of 48
+// the direct form for its one launch (8/8 heads of 64, distance bias: 2 of 48
 // over up to 200 keys 9.4 us against 11.1 gathered, 400 keys 12.1 / 13.6, 800
 // 15.4 / 17.2; 32/8 of 128: 13.3 / 14.0, 18.6 / 16.8, 23.5 / 22.6).
 constexpr int kOneLaunchTiles = 3;
