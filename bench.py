@@ -55,19 +55,19 @@ CSRC = os.path.join(ROOT, "paged_kv_attention_out_gb300", "csrc")
 MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
     "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
-               "sha256": "b84cf1938260e9ec589fab4bbf76bd78b6b2db9e03c21b264ecfcdfe4f363fbd",
-               "bytes": 623414496},
+               "sha256": "ddbb1c342f6986278f999381de1015b62e22f6f458417217a20185a4dd88025b",
+               "bytes": 623428000},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
     "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
                            'pkv_common.cuh'],
                "sha256": "c6b573a0e35b59a562fafa66fbe4c299883b60b354df599b95cacc883e303d6c",
-               "bytes": 493066560},
+               "bytes": 493188256},
     # cascade_prefix_kernel + decode_kernel (suffix) + decode_merge_narrow_kernel,
     # radix-shared decode through cascade decode
     "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
                             'tc_common.cuh', 'pkv_common.cuh'],
-                "sha256": "ecf14c79d6bc6bba35d680eb3bb1a020bb94fc9678a3a1f1215cb636059531fd",
-                "bytes": 372320981},
+                "sha256": "d5c8e64a6a1a73bfe72733e1a0c7634d0a1c0e8b78a6495cc7c6ebd98df571d8",
+                "bytes": 372230187},
 }
 
 

@@ -1,6 +1,8 @@
 """GB300 (sm_103a) paged KV-cache attention: store_kv, paged decode and
-extend attention, and the log-sum-exp merge, as hand-written CUDA kernels
-behind the C ABI of include/pkv.h. This package holds the ctypes binding
+extend attention, the log-sum-exp merge, and beside them the append of normed
+and rotated q, k, v, decode and extend under score rules, and attention of
+drafted token trees, as hand-written CUDA kernels behind the C ABI of
+include/pkv.h. This package holds the ctypes binding
 (same names as the C entry points), the nvcc build and the seeded
 synthetic-input generator used by the tests and the benchmark.
 """
