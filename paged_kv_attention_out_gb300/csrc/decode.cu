@@ -243,6 +243,67 @@ __global__ void __launch_bounds__(kWideWarps * 32) decode_merge_wide_kernel(cons
   if (t == 0 && a.lse) a.lse[bh] = L > 0.f ? ref + logf(L) : -INFINITY;
 }
 
+// Decode under rules and its merge in one launch, for plans of a few splits: the
+// CTAs of a row's splits (of one kv head) are a cluster; each writes its states
+// as above, and after a barrier over the cluster its warps merge a q head each.
+// A launch less for the host (3 rows of up to 600 keys, 8/2 heads of 64: 10.0 us
+// a call from Python instead of 12.2) and no slower on the GPU while every
+// cluster is resident (1 row of 760 keys of 4 kv heads of 64 5.4 / 5.9 us, 4 of
+// up to 760 of 8 kv heads of 128 7.1 / 7.4, up to 2000 10.3 / 9.6); with more,
+// the CTAs of shorter rows wait for their cluster (16 of up to 2000 27.6 / 20.8).
+constexpr int kClusterSplits = 8;
+constexpr int kClusterCtasPerSm = 2;
+
+template <int D, typename Args>
+__global__ void __launch_bounds__(kDecodeThreads, (kDecodeStages <= 3 ? 2 : 1))
+    decode_cluster_kernel(const Args a) {
+  constexpr int kCols = D / 32;  // per lane
+  extern __shared__ __align__(128) uint8_t smem[];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  decode_body<D, kDecodeStages>(a, blockIdx.x, blockIdx.y, blockIdx.z, threadIdx.x, smem,
+                                [] { __syncthreads(); });
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int b = static_cast<int>(blockIdx.z);
+  const int n = row_info(a, b, false).nsplit;
+  if (n <= 1) return;  // written already
+  const int lane = threadIdx.x & 31;
+  for (int g = blockIdx.y * kDecodeWarps + (threadIdx.x >> 5); g < a.group;
+       g += gridDim.y * kDecodeWarps) {
+    const int64_t bh = static_cast<int64_t>(b) * a.hq + blockIdx.x * a.group + g;
+    const float *pl = a.part_lse + bh * a.pstride;
+    const float *po = a.part_o + bh * a.pstride * D + lane * kCols;
+    float lse[kClusterSplits], v[kClusterSplits][kCols], o[kCols];
+#pragma unroll
+    for (int u = 0; u < kClusterSplits; ++u) {
+      lse[u] = u < n ? pl[u] : -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[u][c] = u < n ? po[static_cast<int64_t>(u) * D + c] : 0.f;
+    }
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int u = 0; u < kClusterSplits; ++u) M = fmaxf(M, lse[u]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kClusterSplits; ++u) {
+      const float w = expf(lse[u] - ref);
+      L += w;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[c] += w * v[u][c];
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2)
+      *reinterpret_cast<uint32_t *>(a.o + bh * D + lane * kCols + c) =
+          pack_bf16(o[c] * inv, o[c + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[bh] = L > 0.f ? ref + logf(L) : -INFINITY;
+  }
+}
+
 // The same merge for plans with at most kNarrowStates states per (request,
 // q head) (suffix splits plus cascade prefix slots): a group of D / 16 lanes
 // per pair, 16 columns per lane, 32 / (D / 16) pairs per warp. A quarter of
@@ -467,6 +528,29 @@ static cudaError_t launch_decode_main_d(const Args &a, dim3 grid, cudaStream_t s
                     stream, a);
 }
 
+template <int D, typename Args>
+static cudaError_t launch_decode_cluster_d(const Args &a, dim3 grid, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(decode_cluster_kernel<D, Args>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DecodeSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kDecodeThreads);
+  cfg.dynamicSmemBytes = DecodeSmem<D>::kTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = grid.y;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, decode_cluster_kernel<D, Args>, a);
+}
+
 template <typename Args>
 static cudaError_t launch_decode_main(const Args &a, const PoolGeom &g, const DecodePlan &plan,
                                       int32_t batch, cudaStream_t stream) {
@@ -504,16 +588,20 @@ static cudaError_t launch_decode_rules(const DecodeArgs &base, const ScoreRules 
                                        cudaStream_t stream) {
   DecodeRuleArgs a{base, rules};
   const bool cap = rules.cap_log2 > 0.f, bias = rules.alibi_slopes != nullptr;
-  cudaError_t e;
-  if (cap && bias)
-    e = launch_decode_main(DecodeRulesArgs<kRuleCap | kRuleBias>(a), g, plan, batch, stream);
-  else if (cap)
-    e = launch_decode_main(DecodeRulesArgs<kRuleCap>(a), g, plan, batch, stream);
-  else if (bias)
-    e = launch_decode_main(DecodeRulesArgs<kRuleBias>(a), g, plan, batch, stream);
-  else
-    e = launch_decode_main(DecodeRulesArgs<0>(a), g, plan, batch, stream);
-  if (e != cudaSuccess || plan.splits <= 1) return e;
+  const int64_t ctas = static_cast<int64_t>(batch) * plan.head_groups * plan.splits;
+  const bool cluster = plan.splits > 1 && plan.splits <= kClusterSplits &&
+                       ctas <= kClusterCtasPerSm * static_cast<int64_t>(plan.sm_count);
+  auto main = [&](auto args) {
+    if (!cluster) return launch_decode_main(args, g, plan, batch, stream);
+    const dim3 grid(plan.head_groups, plan.splits, batch);
+    return g.d == 128 ? launch_decode_cluster_d<128>(args, grid, stream)
+                      : launch_decode_cluster_d<64>(args, grid, stream);
+  };
+  const cudaError_t e = cap && bias ? main(DecodeRulesArgs<kRuleCap | kRuleBias>(a))
+                        : cap       ? main(DecodeRulesArgs<kRuleCap>(a))
+                        : bias      ? main(DecodeRulesArgs<kRuleBias>(a))
+                                    : main(DecodeRulesArgs<0>(a));
+  if (e != cudaSuccess || plan.splits <= 1 || cluster) return e;
   const DecodeRulesArgs<0> m(a);
   const int64_t pairs = static_cast<int64_t>(batch) * a.hq;
   if (plan.splits > kMergeBatch && pairs <= kWidePairsPerSm * static_cast<int64_t>(plan.sm_count)) {

@@ -10,20 +10,36 @@
 
 namespace pkv {
 
+// What the host knows of a call.
+struct Sizes {
+  double batch, total_q, keys;  // keys: bound on the requests' keys together
+  double blocks;                // query blocks that hold tokens, about
+  double tiles;                 // key tiles of the longest block
+  bool one_tile;                // a request's tokens fit one query tile, on the average
+  double hkv, d, sms;
+};
+
 // Which of the two forms takes less time, in microseconds, by their measured
-// parts: the longest block (T key tiles, by the hint) bounds the gathered form
-// while there are fewer (block, kv head) pairs N than SMs, the direct one shares
-// the tiles out evenly, at more per tile and with a merge; a hint bounds the
-// longest row, the others are taken to be half as long and more. (Direct /
-// gathered, 32/8 heads of 128, page size 16, distance bias: 1 request of one
-// token over 800 keys 16.3 / 18.4, 4 over up to 800 21.2 / 18.1, over 1400 21.1 /
-// 26.2; 8 over up to 1400 23.8 / 28.6, up to 2000 24.7 / 35.9; 4 of up to 200
-// over up to 1400 33.7 / 31.1, up to 2900 42.1 / 54.3; 8 of up to 200 over up to
-// 1400 48.7 / 35.3. Cap 50 and window 4096: 1 of 1000 over 3000 keys 61 / 49; 4
-// of up to 2048 over up to 8192 251 / 190.)
-static bool direct_is_faster(int64_t pairs, int64_t tiles, int64_t sms) {
-  const double gathered = 12.0 + 1.5 * tiles * ((pairs + sms - 1) / sms);
-  const double direct = 21.5 + 1.5 * static_cast<double>(pairs) * tiles / sms;
+// parts. Gathered: every key is copied (at 5 TB/s; a few us of it are hidden),
+// then the longest block's tiles, or all tiles by the SMs, at 1.5 each. Direct:
+// all tiles and four for each block's beginning and end, shared out evenly, at
+// the copy rate's 1.5 a tile for one query tile and the softmax's 2.2 for two.
+// (Direct / gathered, 32/8 heads of 128, page size 16; distance bias: 1 request
+// of one token over 800 keys 16.3 / 18.4, 4 over up to 800 21.2 / 18.1, 8 over up
+// to 1400 23.8 / 28.6; 64 over up to 16000 316 / 922; 32 of up to 16 over up to
+// 4000 68 / 125; 8 of up to 200 over up to 1400 48.7 / 35.3, 4 over up to 2900
+// 42.1 / 54.3; 4 of up to 512 over up to 16000 177 / 245. Cap 50 and window 4096:
+// that 89 / 81, 64 of one token over up to 16000 184 / 495, 1 of 1000 over 3000
+// 62 / 49, 4 of up to 2048 over up to 8192 251 / 191.)
+static bool direct_is_faster(const Sizes &z) {
+  const double mean = std::max(
+      1.0, std::min(z.tiles, (z.keys - z.total_q / 2) / (z.batch * direct::kN)));
+  const double waves = z.blocks * z.hkv / z.sms;
+  const double copied = 8.0 * z.batch * mean * direct::kN * z.hkv * z.d;  // bytes, both ways
+  const double gathered =
+      12.0 + std::max(0.0, copied / 5e6 - 4.0) + 1.5 * std::max(z.tiles, mean * waves);
+  const double direct =
+      z.one_tile ? 21.5 + 1.5 * (mean + 4) * waves : 26.0 + 2.2 * (mean + 4) * waves;
   return direct < gathered;
 }
 
@@ -46,18 +62,29 @@ size_t extend_direct_workspace(int32_t batch, int32_t total_q, int32_t hq, int32
 }
 
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
-                        int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan) {
-  const int32_t tpb = 2 * (direct::kM / (hq / hkv));
+                        int32_t max_seq, int64_t max_total_keys, int32_t window,
+                        int32_t sm_count, DirectPlan *plan) {
+  const int32_t tpt = direct::kM / (hq / hkv), tpb = 2 * tpt;
   const int64_t blocks = block_bound(batch, total_q, tpb);
   if (batch > direct::kMaxRuleRequests || blocks > direct::kMaxRuleBlocks) return false;
   // key tiles of a block: all up to the longest request's, or the window's
   int64_t tiles = (static_cast<int64_t>(max_seq) + direct::kN - 1) / direct::kN;
   if (window > 0)
     tiles = std::min<int64_t>(tiles, (static_cast<int64_t>(window) + tpb) / direct::kN + 2);
-  const int64_t busy = std::max<int64_t>(batch, (static_cast<int64_t>(total_q) + tpb - 1) / tpb);
   *plan = direct::plan(static_cast<int32_t>(blocks), 2, hkv, d, max_seq, tiles, sm_count);
-  return (plan->whole && tiles <= kOneLaunchTiles) ||
-         direct_is_faster(busy * hkv, tiles, sm_count > 0 ? sm_count : 1);
+  if (plan->whole && tiles <= kOneLaunchTiles) return true;
+  Sizes z;
+  z.batch = batch;
+  z.total_q = total_q;
+  z.keys = static_cast<double>(batch) * max_seq;
+  if (max_total_keys >= 1) z.keys = std::min(z.keys, static_cast<double>(max_total_keys));
+  z.blocks = std::max<double>(batch, (static_cast<int64_t>(total_q) + tpb - 1) / tpb);
+  z.tiles = static_cast<double>(tiles);
+  z.one_tile = total_q <= static_cast<int64_t>(batch) * tpt;
+  z.hkv = hkv;
+  z.d = d;
+  z.sms = sm_count > 0 ? sm_count : 1;
+  return direct_is_faster(z);
 }
 
 cudaError_t launch_extend_direct(const PoolGeom &g, int32_t layer, const void *q,

@@ -605,7 +605,7 @@ static pkv_status extend_call(const pkv_pool *pool, int32_t layer, const void *q
     if ((s = device_info(&d)) != PKV_OK) return s;
     pkv::DirectPlan plan;
     if (pkv::extend_direct_plan(batch, total_q, num_q_heads, g.hkv, g.d,
-                                static_cast<int32_t>(cap),
+                                static_cast<int32_t>(cap), max_total_keys_hint,
                                 rules.prefix_lens ? 0 : rules.window, d->sm_count, &plan)) {
       if (!plan.whole &&
           (s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)

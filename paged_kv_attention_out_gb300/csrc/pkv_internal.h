@@ -180,7 +180,8 @@ cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const i
 // rules' (0 for none, or where a prefix adds to it). false: more blocks or
 // requests than it takes, or the form of extend.cu is faster.
 bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
-                        int32_t max_seq, int32_t window, int32_t sm_count, DirectPlan *plan);
+                        int32_t max_seq, int64_t max_total_keys, int32_t window,
+                        int32_t sm_count, DirectPlan *plan);
 // Its workspace, for any window.
 size_t extend_direct_workspace(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
                                int32_t max_seq, int32_t sm_count);
