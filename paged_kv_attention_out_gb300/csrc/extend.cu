@@ -13,7 +13,7 @@
 //       the pool once per call. The runs of the requests lie back to back in
 //       request order, [2][Hkv][cap_rows][D], so the workspace is sized by the
 //       keys present (a host bound on their sum), not by batch x max length;
-//       two waves of resident CTAs loop over 16-row chunks of that space,
+//       two waves of resident CTAs loop over chunks of that space,
 //       finding each chunk's request by a prefix sum of the rounded lengths;
 //       the first CTA builds the block schedule meanwhile; pool rows are
 //       read with an L2 evict-first policy and the workspace rows written
@@ -174,7 +174,12 @@ struct ExtendRulesArgs : ExtendRuleArgs {
   explicit ExtendRulesArgs(const ExtendRuleArgs &a) : ExtendRuleArgs(a) {}
 };
 
-constexpr int kGatherKeys = 16;     // keys per chunk of a gather CTA (two per warp)
+// Keys per chunk of a gather CTA: two per warp, or one where that leaves no CTA
+// of the grid waiting (a warp's keys are copied one after the other): 1 chunk of
+// 512 tokens, 32/8 heads of 128, 16.8 us a call instead of 17.9; 2 of up to 1002
+// of 64 19.7, 22.0.
+constexpr int kGatherKeys = 16;
+constexpr int kGatherKeysFew = 8;
 constexpr int kGatherWaves = 2;     // copying CTAs: this many waves of resident CTAs
 constexpr int kGatherThreads = 256;
 
@@ -200,6 +205,7 @@ __device__ __forceinline__ int64_t run_rows(const GatherArgs &a, int seq) {
 // entries); then (request, first token, cost) per block in request order;
 // then the sorted (request, first token) pairs; then off_r per request.
 constexpr int kPlanHist = 16;
+constexpr int kSharedBuckets = 1024;  // a histogram of at most these is in shared memory
 
 __host__ __device__ inline int64_t plan_ints(int64_t batch, int64_t nbuck, int64_t max_blocks) {
   return kPlanHist + nbuck + 5 * max_blocks + batch;
@@ -236,13 +242,16 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
 template <bool kRules>
 __device__ void plan_blocks(const GatherArgs &a) {
   __shared__ int s_first_bad;
-  __shared__ int s_part[kGatherThreads];
+  __shared__ int s_end[kGatherThreads];  // per request of a round: its blocks' end,
+  __shared__ int s_c[kGatherThreads];    // chunk tokens and cached prefix
+  __shared__ int s_p[kGatherThreads];
+  __shared__ int s_hist[kSharedBuckets];
   __shared__ int64_t s_warp[kGatherThreads / 32];
   const int tid = threadIdx.x;
   const int per = 2 * a.tokens_per_tile;
   const int nbuck = a.nbuck;
-  int *hist = a.plan + kPlanHist;
-  int *ent = hist + nbuck;                // 3 per block, request order
+  int *ent = a.plan + kPlanHist + nbuck;  // 3 per block, request order
+  int *hist = nbuck <= kSharedBuckets ? s_hist : a.plan + kPlanHist;
   int *sorted = ent + 3 * a.max_blocks;   // 2 per block, by cost
   int *offsets = a.plan + plan_offsets(nbuck, a.max_blocks);
   if (tid == 0) s_first_bad = a.batch;
@@ -285,36 +294,38 @@ __device__ void plan_blocks(const GatherArgs &a) {
       if (r < nreq && p >= 0 && rows > 0 && placed) nb = (c + per - 1) / per;
     }
     run_base += round_rows;
-    s_part[tid] = nb;
+    int64_t round_blocks;
+    s_end[tid] = static_cast<int>(block_scan(nb, s_warp, &round_blocks));
+    s_c[tid] = c;
+    s_p[tid] = p;
     __syncthreads();
-    for (int off = 1; off < kGatherThreads; off <<= 1) {  // inclusive scan
-      const int v = tid >= off ? s_part[tid - off] : 0;
-      __syncthreads();
-      s_part[tid] += v;
-      __syncthreads();
-    }
-    const int first = base + s_part[tid] - nb;
-    for (int i = 0; i < nb; ++i) {
-      const int j0 = i * per;
-      const int tokens = min(per, c - j0);
+    // the round's blocks, one per thread at a time
+    for (int i = tid; i < static_cast<int>(round_blocks); i += kGatherThreads) {
+      int j = 0;  // its request: the first whose blocks end after i
+#pragma unroll
+      for (int step = kGatherThreads / 2; step > 0; step >>= 1)
+        j += s_end[j + step - 1] <= i ? step : 0;
+      const int j0 = (i - (j > 0 ? s_end[j - 1] : 0)) * per;
+      const int bc = s_c[j], bp = s_p[j];
+      const int tokens = min(per, bc - j0);
       const int tok0 = min(a.tokens_per_tile, tokens);
       const int tok1 = max(0, tokens - a.tokens_per_tile);
-      int n0 = (p + j0 + tok0 + 127) / 128;
-      int n1 = tok1 == 0 ? 0 : (p + j0 + a.tokens_per_tile + tok1 + 127) / 128;
+      int n0 = (bp + j0 + tok0 + 127) / 128;
+      int n1 = tok1 == 0 ? 0 : (bp + j0 + a.tokens_per_tile + tok1 + 127) / 128;
       if (kRules) {
-        const int pre = rule_prefix(a.prefix_lens, r, p + c);
-        const int gap = tile_walk(p + j0, a.window, pre).gap;
+        const int pre = rule_prefix(a.prefix_lens, r0 + j, bp + bc);
+        const int gap = tile_walk(bp + j0, a.window, pre).gap;
         n0 = max(n0, (pre + 127) / 128) - gap;
         n1 = tok1 == 0 ? 0 : max(n1, (pre + 127) / 128) - gap;
       }
       const int cost = min(n0 + n1 + 2, nbuck - 1);
-      const int b = first + i;
-      ent[3 * b] = r;
-      ent[3 * b + 1] = j0;
-      ent[3 * b + 2] = cost;
+      const int blk = base + i;
+      ent[3 * blk] = r0 + j;
+      ent[3 * blk + 1] = j0;
+      ent[3 * blk + 2] = cost;
       atomicAdd(&hist[cost], 1);
     }
-    base += s_part[kGatherThreads - 1];
+    base += static_cast<int>(round_blocks);
     __syncthreads();
   }
   const int nblk = base;
@@ -326,15 +337,8 @@ __device__ void plan_blocks(const GatherArgs &a) {
     const int k = nbuck - 1 - (tid * run + i);
     if (k >= 0) sum += hist[k];
   }
-  s_part[tid] = sum;
-  __syncthreads();
-  for (int off = 1; off < kGatherThreads; off <<= 1) {
-    const int v = tid >= off ? s_part[tid - off] : 0;
-    __syncthreads();
-    s_part[tid] += v;
-    __syncthreads();
-  }
-  int start = s_part[tid] - sum;
+  int64_t all;
+  int start = static_cast<int>(block_scan(sum, s_warp, &all)) - sum;
   for (int i = 0; i < run; ++i) {
     const int k = nbuck - 1 - (tid * run + i);
     if (k >= 0) {
@@ -359,17 +363,17 @@ __device__ void plan_blocks(const GatherArgs &a) {
 // the plain gather keeps its lean inner loop.
 // kRules: rows outside every query's window and the prefix are not read (nor,
 // for key tiles without any other row, written).
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 __device__ __forceinline__ void gather_body(const GatherArgs &a);
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos);
 
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 __global__ void __launch_bounds__(kGatherThreads)
     extend_gather_kernel(const GatherArgs a) {
   grid_dependency_wait();  // the chunk's K/V may come from the previous kernel (store_kv)
   grid_dependents_launch();
-  gather_body<D, kStore, kRules>(a);
+  gather_body<D, kStore, kRules, kKeys>(a);
 }
 
 // Read-only 16-byte load / 16-byte store with an L2 eviction-priority
@@ -394,24 +398,24 @@ __device__ __forceinline__ uint64_t l2_evict_last_policy() {
 }
 
 // The first CTA builds the schedule (dispatched before the copying CTAs);
-// the others copy 16-row chunks of the key space, chunk c by CTA 1 + c mod
+// the others copy chunks of kKeys rows of the key space, chunk c by CTA 1 + c mod
 // (grid - 1), so a grid of whole waves finishes together.
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 __device__ __forceinline__ void gather_body(const GatherArgs &a) {
   if (blockIdx.x == 0) {
     plan_blocks<kRules>(a);
     return;
   }
-  const int64_t chunks = a.cap_rows / kGatherKeys;
+  const int64_t chunks = a.cap_rows / kKeys;
   for (int64_t c = blockIdx.x - 1; c < chunks; c += gridDim.x - 1)
-    if (!gather_rows<D, kStore, kRules>(a, c * kGatherKeys)) break;
+    if (!gather_rows<D, kStore, kRules, kKeys>(a, c * kKeys)) break;
 }
 
-// Copies rows pos .. pos + 15 of the key space. Returns false once pos lies
+// Copies rows pos .. pos + kKeys - 1 of the key space. Returns false once pos lies
 // past every run (so does every later chunk).
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
-  // The request whose run holds these 16 rows (runs are multiples of 128
+  // The request whose run holds these rows (runs are multiples of 128
   // rows, so they never straddle two requests): the same scan of the
   // rounded lengths as the planner's, kGatherThreads requests per round.
   __shared__ int64_t s_warp[kGatherThreads / 32];
@@ -479,7 +483,7 @@ __device__ __forceinline__ bool gather_rows(const GatherArgs &a, int64_t pos) {
   constexpr int kUnroll = 4;  // chunks per lane per row in flight (x 2 rows)
   const uint64_t pol_read = l2_evict_first_policy();
   const uint64_t pol_write = l2_evict_last_policy();
-  for (int kk = warp; kk < kGatherKeys; kk += kGatherThreads / 32) {
+  for (int kk = warp; kk < kKeys; kk += kGatherThreads / 32) {
     const int key = key0 + kk;
     // the key's K row (c = 0) and V row (c = 1) are copied together
     const uint4 *src[2] = {nullptr, nullptr};
@@ -1186,12 +1190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Copying CTAs of one gather variant resident on an SM at once (looked up
 // once per variant).
-template <int D, bool kStore, bool kRules>
+template <int D, bool kStore, bool kRules, int kKeys>
 int gather_ctas_per_sm() {
   static const int n = [] {
     int b = 0;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-               &b, extend_gather_kernel<D, kStore, kRules>, kGatherThreads, 0) == cudaSuccess &&
+               &b, extend_gather_kernel<D, kStore, kRules, kKeys>, kGatherThreads, 0) ==
+                       cudaSuccess &&
                    b > 0
                ? b
                : 1;
@@ -1200,15 +1205,22 @@ int gather_ctas_per_sm() {
 }
 
 // The planner, then two waves of copying CTAs (twice as many as are resident
-// at once) looping over the 16-row chunks.
+// at once) looping over the chunks.
+template <int D, bool kStore, bool kRules, int kKeys>
+cudaError_t launch_gather_keys(const GatherArgs &ga, int64_t resident, cudaStream_t stream) {
+  const int64_t copiers = std::min<int64_t>(ga.cap_rows / kKeys, resident * kGatherWaves);
+  return launch_pdl(extend_gather_kernel<D, kStore, kRules, kKeys>,
+                    dim3(static_cast<unsigned>(1 + copiers)), dim3(kGatherThreads), 0, stream, ga);
+}
 template <int D, bool kStore, bool kRules>
 cudaError_t launch_gather(const GatherArgs &ga, int32_t sm_count, cudaStream_t stream) {
-  const int64_t chunks = ga.cap_rows / kGatherKeys;
-  const int64_t copiers = std::min<int64_t>(
-      chunks, static_cast<int64_t>(sm_count) * gather_ctas_per_sm<D, kStore, kRules>() *
-                  kGatherWaves);
-  return launch_pdl(extend_gather_kernel<D, kStore, kRules>,
-                    dim3(static_cast<unsigned>(1 + copiers)), dim3(kGatherThreads), 0, stream, ga);
+  const int64_t few = static_cast<int64_t>(sm_count) *
+                      gather_ctas_per_sm<D, kStore, kRules, kGatherKeysFew>();
+  if (ga.cap_rows / kGatherKeysFew < few)
+    return launch_gather_keys<D, kStore, kRules, kGatherKeysFew>(ga, few, stream);
+  return launch_gather_keys<D, kStore, kRules, kGatherKeys>(
+      ga, static_cast<int64_t>(sm_count) * gather_ctas_per_sm<D, kStore, kRules, kGatherKeys>(),
+      stream);
 }
 
 template <int D, typename Args>
