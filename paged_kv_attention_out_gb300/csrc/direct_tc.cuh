@@ -154,6 +154,7 @@ struct DirectArgs {
   int32_t hq;
   int32_t group;
   int32_t tokens_per_tile;
+  int32_t tokens_per_block;  // one or two query tiles' (kQT = 2)
   int32_t max_tree;        // tree
   int32_t blocks_per_req;  // tree
   int32_t read_once;       // no K/V byte is read by more than one block
@@ -232,7 +233,7 @@ __device__ __forceinline__ Block load_block(const DirectArgs &a, const Blocks &b
   k.seq = a.seq_lens[k.req];
   k.c = end - beg;
   k.p = k.seq - k.c;
-  const int tpb = kQT * a.tokens_per_tile;
+  const int tpb = a.tokens_per_block;
   const unsigned bad = bad_request<kRules>(a, k.req, beg, end, k.seq);
   if (bad) {
     if (report && k.sub == 0) flag_error(a.err, bad);
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
   const int lane = tid & 31;
   const int kvh = blockIdx.x;
   const int tpt = a.tokens_per_tile;
-  const int tpb = kQT * tpt;
+  const int tpb = a.tokens_per_block;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1332,7 +1333,7 @@ cudaError_t launch(const DirectArgs &a, const CUtensorMap &km, const CUtensorMap
 
 // In key tiles: what the search for a share, the partial states and the second
 // kernel cost a call (about 6 us), and what a further block in a share costs it.
-constexpr int share_cost(int query_tiles) { return query_tiles == 1 ? 8 : 6; }
+constexpr int share_cost(int tiles_per_block) { return tiles_per_block == 1 ? 8 : 6; }
 constexpr int kFurtherBlock = 8;
 
 // Groups of a call of at most `blocks` query blocks, each of at most
@@ -1347,10 +1348,11 @@ constexpr int kFurtherBlock = 8;
 // 16.2, of 1400 17.3 / 15.4; 16 of up to 2000 25.1 / 30.2, of 2900 31.4 / 31.6;
 // 64 drafts: 1 of 520 17.8 / 18.8, of 900 22.2 / 20.6; 16 of up to 2000 38.4 /
 // 39.2, of 2900 47.7 / 37.5.
-inline DirectPlan plan(int32_t blocks, int32_t query_tiles, int32_t hkv, int32_t d,
-                       int32_t max_seq, int64_t block_tiles, int32_t sm_count) {
+inline DirectPlan plan(int32_t blocks, int32_t query_tiles, int32_t tiles_per_block, int32_t hkv,
+                       int32_t d, int32_t max_seq, int64_t block_tiles, int32_t sm_count) {
   DirectPlan p{};
   p.query_tiles = query_tiles;
+  p.tiles_per_block = tiles_per_block;
   p.max_blocks = blocks;
   // one group per Hkv SMs, and no more than there are smallest shares
   const int64_t all = std::max<int64_t>(1, (sm_count > 0 ? sm_count : 1) / hkv);
@@ -1366,7 +1368,7 @@ inline DirectPlan plan(int32_t blocks, int32_t query_tiles, int32_t hkv, int32_t
     p.workspace_bytes = p.table_offset + sizeof(int4) * static_cast<size_t>(blocks);
   }
   if (blocks <= all &&
-      2 * all * (block_tiles - share_cost(query_tiles)) <=
+      2 * all * (block_tiles - share_cost(tiles_per_block)) <=
           blocks * (block_tiles + kFurtherBlock)) {
     p.whole = 1;
     p.groups = blocks;
@@ -1400,6 +1402,7 @@ inline bool direct_args(DirectArgs *out, CUtensorMap *km, CUtensorMap *vm, CUten
   a.hq = hq;
   a.group = hq / g.hkv;
   a.tokens_per_tile = kM / a.group;
+  a.tokens_per_block = plan.tiles_per_block * a.tokens_per_tile;
   a.max_blocks = plan.max_blocks;
   a.groups = plan.groups;
   a.whole = plan.whole;

@@ -43,10 +43,16 @@ static bool direct_is_faster(const Sizes &z) {
   return direct < gathered;
 }
 
-// A call whose blocks have a group each and no more key tiles than this takes
-// the direct form for its one launch (8/8 heads of 64, distance bias: 2 of 48
-// over up to 200 keys 9.4 us against 11.1 gathered, 400 keys 12.1 / 13.6, 800
-// 15.4 / 17.2; 32/8 of 128: 13.3 / 14.0, 18.6 / 16.8, 23.5 / 22.6).
+// A call whose blocks have a group each takes the direct form with one query
+// tile to a block (both softmax groups walk it), or with two where those do not
+// fit but the key tiles are no more than kOneLaunchTiles: one launch, no shares,
+// no copy. (Blocks of one tile, direct / of two / gathered, distance bias: 1 of
+// 200 tokens over 1000 keys, 32/8 heads of 128, 18.4 / 24.8 / 23.8 us; 4 of up to
+// 200 over up to 1600, 16/16 of 64, 18.3 / 30.2 / 29.3; 2 of up to 300 over up to
+// 1500, 32/8 of 128, 23.8 / 34.8 / 32.5; 2 of 48 over up to 200, 8/8 of 64, 9.4 /
+// 9.4 / 11.1. Of two: 3 tiles 12.1 / 13.6 gathered, 4 13.3 / 14.0, 7 23.5 / 22.6.
+// Shared out, one tile to a block is the slower: 4 of up to 512 over up to 16000
+// 224 / 176.)
 constexpr int kOneLaunchTiles = 3;
 
 static int64_t block_bound(int32_t batch, int32_t total_q, int32_t tpb) {
@@ -56,7 +62,7 @@ static int64_t block_bound(int32_t batch, int32_t total_q, int32_t tpb) {
 size_t extend_direct_workspace(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
                                int32_t max_seq, int32_t sm_count) {
   const int64_t blocks = block_bound(batch, total_q, 2 * (direct::kM / (hq / hkv)));
-  return direct::plan(static_cast<int32_t>(std::min<int64_t>(blocks, direct::kMaxRuleBlocks)), 2,
+  return direct::plan(static_cast<int32_t>(std::min<int64_t>(blocks, direct::kMaxRuleBlocks)), 2, 2,
                       hkv, d, max_seq, 0, sm_count)
       .workspace_bytes;
 }
@@ -65,14 +71,20 @@ bool extend_direct_plan(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv,
                         int32_t max_seq, int64_t max_total_keys, int32_t window,
                         int32_t sm_count, DirectPlan *plan) {
   const int32_t tpt = direct::kM / (hq / hkv), tpb = 2 * tpt;
-  const int64_t blocks = block_bound(batch, total_q, tpb);
-  if (batch > direct::kMaxRuleRequests || blocks > direct::kMaxRuleBlocks) return false;
-  // key tiles of a block: all up to the longest request's, or the window's
-  int64_t tiles = (static_cast<int64_t>(max_seq) + direct::kN - 1) / direct::kN;
-  if (window > 0)
-    tiles = std::min<int64_t>(tiles, (static_cast<int64_t>(window) + tpb) / direct::kN + 2);
-  *plan = direct::plan(static_cast<int32_t>(blocks), 2, hkv, d, max_seq, tiles, sm_count);
-  if (plan->whole && tiles <= kOneLaunchTiles) return true;
+  if (batch > direct::kMaxRuleRequests) return false;
+  int64_t tiles = 0;
+  for (int32_t n = 1; n <= 2; ++n) {  // query tiles to a block
+    const int64_t blocks = block_bound(batch, total_q, n * tpt);
+    if (blocks > direct::kMaxRuleBlocks) continue;
+    // key tiles of a block: all up to the longest request's, or the window's
+    tiles = (static_cast<int64_t>(max_seq) + direct::kN - 1) / direct::kN;
+    if (window > 0)
+      tiles = std::min<int64_t>(tiles,
+                                (static_cast<int64_t>(window) + n * tpt) / direct::kN + 2);
+    *plan = direct::plan(static_cast<int32_t>(blocks), 2, n, hkv, d, max_seq, tiles, sm_count);
+    if (plan->whole && (n == 1 || tiles <= kOneLaunchTiles)) return true;
+  }
+  if (block_bound(batch, total_q, tpb) > direct::kMaxRuleBlocks) return false;
   Sizes z;
   z.batch = batch;
   z.total_q = total_q;

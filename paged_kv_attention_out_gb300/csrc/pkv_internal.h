@@ -158,6 +158,7 @@ cudaError_t launch_extend(const PoolGeom &g, int32_t layer, const void *q,
 // bytes for one group), all from host scalars.
 struct DirectPlan {
   int32_t query_tiles;
+  int32_t tiles_per_block;  // query tiles' tokens in a block
   int32_t max_blocks;
   int32_t groups;
   int32_t whole;  // a group per block, nothing shared

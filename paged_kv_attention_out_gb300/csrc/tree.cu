@@ -37,7 +37,7 @@ DirectPlan tree_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t 
                      int32_t max_seq, int32_t sm_count) {
   int32_t query_tiles;
   const int32_t per_req = tree_blocks(hq, hkv, max_tree, &query_tiles);
-  return direct::plan(batch * per_req, query_tiles, hkv, d, max_seq,
+  return direct::plan(batch * per_req, query_tiles, query_tiles, hkv, d, max_seq,
                       (static_cast<int64_t>(max_seq) + kN - 1) / kN, sm_count);
 }
 
