@@ -56,18 +56,18 @@ MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
     "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
                "sha256": "61dd1c44d2f27e6e6de49e35638038c88851931c7dc5a5017231c2ec3a3dc961",
-               "bytes": 623419776},
+               "bytes": 623410752},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
     "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
                            'pkv_common.cuh'],
-               "sha256": "c6b573a0e35b59a562fafa66fbe4c299883b60b354df599b95cacc883e303d6c",
-               "bytes": 491062976},
+               "sha256": "a8fcda746c45520e1c6368beac1fc56fb289e0f28797bb412fe52514766073b6",
+               "bytes": 492738240},
     # cascade_prefix_kernel + decode_kernel (suffix) + decode_merge_narrow_kernel,
     # radix-shared decode through cascade decode
     "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
                             'tc_common.cuh', 'pkv_common.cuh'],
                 "sha256": "cf48a4c01fddc2cc57e0856dbf77fdbf05ecb8fdaa6b135c94e5219da14c5e83",
-                "bytes": 372233429},
+                "bytes": 372185685},
 }
 
 

@@ -162,14 +162,13 @@ def _contig(t: torch.Tensor, name: str):
 # The calls below are launch-bound at decode sizes, so each tensor is checked by
 # one short expression; what is wrong is found out only when something is.
 _bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
-
-
-def _device() -> int:
-    return torch._C._cuda_getDevice()  # torch.cuda.current_device without its lazy set-up
+# torch.cuda.current_device without its lazy set-up (None in a torch without CUDA)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _handle(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _refuse(t, dtype, ndim: int, dev: int, name: str):
@@ -209,19 +208,22 @@ def _pool_arg(pool, dev: int) -> PkvPool:
     return PkvPool(base, L, NP, P, H, D)
 
 
-def _queries(q, o, lse, dev: int):
-    """Addresses of q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None)."""
-    shape = q.shape
+def _queries(q, o, lse, ps: PkvPool, dev: int):
+    """Addresses of q, o [T, Hq, D] bf16 and lse [T, Hq] fp32 (or None), then T and Hq."""
     qp = _arg(q, _bf16, 3, dev, "q")
     op = _arg(o, _bf16, 3, dev, "o")
+    shape = q.shape
     if o.shape != shape:
         raise ValueError("o must match q")
+    t, hq, d = shape
+    if d != ps.head_dim:
+        raise ValueError("q must have the pool's head_dim")
     if lse is None:
-        return qp, op, None
+        return qp, op, None, t, hq
     lp = _arg(lse, _f32, 2, dev, "lse")
-    if lse.shape != shape[:2]:
+    if lse.shape != (t, hq):
         raise ValueError("lse must be [T, Hq]")
-    return qp, op, lp
+    return qp, op, lp, t, hq
 
 
 def _tables(page_table, seq_lens, table_idx, batch: int, dev: int):
@@ -229,23 +231,18 @@ def _tables(page_table, seq_lens, table_idx, batch: int, dev: int):
     table's stride."""
     pp = _arg(page_table, _i32, 2, dev, "page_table")
     rows, stride = page_table.shape
-    sp = _arg(seq_lens, _i32, 1, dev, "seq_lens")
-    if seq_lens.shape[0] != batch:
-        raise ValueError("seq_lens must have batch entries")
+    sp = _ints(seq_lens, batch, dev, "seq_lens")
     if table_idx is None:
         if rows < batch:
             raise ValueError("page_table must have a row per request")
         return pp, sp, None, stride
-    tp = _arg(table_idx, _i32, 1, dev, "table_idx")
-    if table_idx.shape[0] != batch:
-        raise ValueError("table_idx must have batch entries")
-    return pp, sp, tp, stride
+    return pp, sp, _ints(table_idx, batch, dev, "table_idx"), stride
 
 
 def _ints(t, n: int, dev: int, name: str) -> int:
     """Address of an int32 tensor of n entries."""
     p = _arg(t, _i32, 1, dev, name)
-    if t.shape[0] != n:
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries")
     return p
 
@@ -256,8 +253,9 @@ def _workspace(workspace, dev: int):
         return None, 0
     if workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, the current device is cuda:{dev}")
-    _contig(workspace, "workspace")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def pool_struct(pool: torch.Tensor) -> PkvPool:
@@ -320,11 +318,11 @@ def pkv_norm_rope_kv_store(pool, layer: int, q, k, v, q_out, positions, out_loc,
         pp = _ints(positions, n, dev, "positions")
     if q_norm is not None:
         qn = _arg(q_norm, _bf16, 1, dev, "q_norm")
-        if q_norm.shape[0] != d:
+        if q_norm.numel() != d:
             raise ValueError("q_norm must have head_dim entries")
     if k_norm is not None:
         kn = _arg(k_norm, _bf16, 1, dev, "k_norm")
-        if k_norm.shape[0] != d:
+        if k_norm.numel() != d:
             raise ValueError("k_norm must have head_dim entries")
     _check(load().pkv_norm_rope_kv_store(
         ctypes.byref(ps), int(layer), qp, qs, op, hq, kp, vp, ks, qn, kn, float(eps), tp, rows, rot,
@@ -393,10 +391,7 @@ def pkv_paged_decode_attn_mod(pool, layer: int, q, o, lse, page_table, seq_lens,
     request sees (min(seq_len, window + prefix) with a window)."""
     dev = _device()
     ps = _pool_arg(pool, dev)
-    qp, op, lp = _queries(q, o, lse, dev)
-    B, Hq, D = q.shape
-    if D != ps.head_dim:
-        raise ValueError("q must have the pool's head_dim")
+    qp, op, lp, B, Hq = _queries(q, o, lse, ps, dev)
     pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
     mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
     ws, ws_bytes = _workspace(workspace, dev)
@@ -528,11 +523,8 @@ def pkv_paged_extend_attn_mod(pool, layer: int, q, qo_indptr, o, lse, page_table
     prefix see the keys behind them."""
     dev = _device()
     ps = _pool_arg(pool, dev)
-    qp, op, lp = _queries(q, o, lse, dev)
-    T, Hq, D = q.shape
-    if D != ps.head_dim:
-        raise ValueError("q must have the pool's head_dim")
-    B = seq_lens.shape[0]
+    qp, op, lp, T, Hq = _queries(q, o, lse, ps, dev)
+    B = seq_lens.numel()
     pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
     mod = _score_mod(soft_cap, alibi_slopes, window, prefix_lens, B, Hq, dev)
     ws, ws_bytes = _workspace(workspace, dev)
@@ -598,11 +590,8 @@ def pkv_paged_tree_attn(pool, layer: int, q, qo_indptr, parents, o, lse, page_ta
     drafted tokens, whose keys are in the pool."""
     dev = _device()
     ps = _pool_arg(pool, dev)
-    qp, op, lp = _queries(q, o, lse, dev)
-    T, Hq, D = q.shape
-    if D != ps.head_dim:
-        raise ValueError("q must have the pool's head_dim")
-    B = seq_lens.shape[0]
+    qp, op, lp, T, Hq = _queries(q, o, lse, ps, dev)
+    B = seq_lens.numel()
     pp, sp, tp, stride = _tables(page_table, seq_lens, table_idx, B, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _check(load().pkv_paged_tree_attn(
