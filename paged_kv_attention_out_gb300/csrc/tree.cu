@@ -24,21 +24,37 @@ cudaError_t launch_d(const DirectArgs &a, const DirectPlan &plan, bool tma, cons
              : launch<D, 2, false, 0>(a, km, vm, qm, stream);
 }
 
-int32_t tree_blocks(int32_t hq, int32_t hkv, int32_t max_tree, int32_t *query_tiles) {
-  const int32_t tpt = kM / (hq / hkv);
-  *query_tiles = max_tree <= tpt ? 1 : 2;
-  const int32_t tpb = *query_tiles * tpt;
-  return (max_tree + tpb - 1) / tpb;  // per request
+// Blocks per request.
+int32_t tree_blocks(int32_t hq, int32_t hkv, int32_t max_tree, int32_t tiles_per_block) {
+  const int32_t tpb = tiles_per_block * (kM / (hq / hkv));
+  return (max_tree + tpb - 1) / tpb;
 }
 
 }  // namespace
 
+// One query tile where it holds a request's drafts, or where every query tile
+// can have a group of its own and the keys, which its other tiles read again,
+// stay in L2; otherwise two. (64 drafts, blocks of one / two tiles, page size 16;
+// 32/8 heads of 128: 1 request of 520 keys 12.9 / 18.6 us, of 1400 18.3 / 18.9, 4
+// of up to 900 15.8 / 22.9, 2 of up to 2900 20.3 / 25.4, 8 of up to 2900 32.6 /
+// 32.4; 28/4 of 64: 4 of up to 2900 18.4 / 21.7.)
+constexpr int64_t kReadTwice = 64 << 20;
+
 DirectPlan tree_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t d, int32_t max_tree,
                      int32_t max_seq, int32_t sm_count) {
-  int32_t query_tiles;
-  const int32_t per_req = tree_blocks(hq, hkv, max_tree, &query_tiles);
-  return direct::plan(batch * per_req, query_tiles, query_tiles, hkv, d, max_seq,
-                      (static_cast<int64_t>(max_seq) + kN - 1) / kN, sm_count);
+  const int64_t tiles = (static_cast<int64_t>(max_seq) + kN - 1) / kN;
+  auto plan = [&](int32_t query_tiles, int32_t tiles_per_block) {
+    return direct::plan(batch * tree_blocks(hq, hkv, max_tree, tiles_per_block), query_tiles,
+                        tiles_per_block, hkv, d, max_seq, tiles, sm_count);
+  };
+  const DirectPlan one = plan(1, 1);
+  if (max_tree <= kM / (hq / hkv)) return one;
+  const DirectPlan two = plan(2, 2);
+  const int64_t kv_bytes = 4 * batch * tiles * kN * hkv * d;
+  const bool few = one.max_blocks * static_cast<int64_t>(hkv) <= sm_count && kv_bytes <= kReadTwice;
+  DirectPlan p = one.whole || few ? one : two;
+  p.workspace_bytes = std::max(one.workspace_bytes, two.workspace_bytes);  // (grows with the sizes)
+  return p;
 }
 
 cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const int32_t *qo_indptr,
@@ -54,10 +70,9 @@ cudaError_t launch_tree(const PoolGeom &g, int32_t layer, const void *q, const i
                    table_stride, table_idx, seq_lens, batch, total_q, hq, scale, plan, workspace,
                    err))
     return cudaErrorInvalidValue;
-  int32_t query_tiles;
   a.parents = parents;
   a.max_tree = max_tree;
-  a.blocks_per_req = tree_blocks(hq, g.hkv, max_tree, &query_tiles);
+  a.blocks_per_req = tree_blocks(hq, g.hkv, max_tree, plan.tiles_per_block);
   a.read_once = a.blocks_per_req == 1;
   return g.d == 128 ? launch_d<128>(a, plan, tma, km, vm, qm, stream)
                     : launch_d<64>(a, plan, tma, km, vm, qm, stream);
