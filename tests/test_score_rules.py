@@ -358,6 +358,17 @@ def test_decode_of_long_rows_merges_many_states(D, Hq, Hkv, rule):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rule", [dict(cap=20.0), dict(alibi=True, prefix=[200, 0]),
+                                  dict(cap=2.0, alibi=True, window=900), dict(window=2500)], ids=str)
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 7)])
+def test_extend_with_blocks_shared_by_groups(D, P, rule):
+    """More blocks than groups and long rows: blocks of one and of two query tiles, cut and merged."""
+    case = W.random_case(20, kind="extend", seq_lens=[3900, 2000, 300, 1500, 800, 3000],
+                         chunk_lens=[150, 130, 20, 3, 140, 129], Hq=16, Hkv=16, D=D, P=P)
+    mod_check(Rules(case, **rule))
+
+
+@pytest.mark.gpu
 def test_a_chunked_prompt_equals_the_whole():
     """A prefix-LM prompt in one chunk, and its causal rest in two: the second chunk sees the
     prefix that the first one stored."""

@@ -115,6 +115,20 @@ def test_long_caches_are_shared_by_groups(P, drafts):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P", [1, 16, 7])
+@pytest.mark.parametrize("Hq,Hkv,B,most", [(8, 2, 39, 64), (28, 4, 20, 36)])
+@pytest.mark.parametrize("longest", [300, 2900])
+def test_two_query_tiles_to_a_block(D, P, Hq, Hkv, B, most, longest):
+    """More query tiles than groups: two to a block, a block to a group (short rows) or shared."""
+    rng = np.random.default_rng(B + longest)
+    drafts = [most, 1, most // 2, most // 2 + 1, 0] + list(rng.integers(1, most + 1, B - 5))
+    cached = [longest, 0, 128, 127, 40] + list(rng.integers(0, 300, B - 5))
+    case, parents = tree_case(16, cached, drafts, Hq=Hq, Hkv=Hkv, D=D, P=P)
+    tree_check(case, parents)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("hint", [0, 100, 100000])
 def test_the_hint_changes_only_the_schedule(hint):
     case, parents = tree_case(8, [900, 20, 333], [6, 7, 1], Hq=8, Hkv=2, D=64, P=16)
