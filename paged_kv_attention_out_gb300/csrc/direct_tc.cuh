@@ -966,14 +966,15 @@ __global__ void __launch_bounds__((4 * kQT + 1 + producer_warps(kQT, kTma)) * 32
           }
         }
         if (masked || a.q_mode || ((kCap || kBias) && !near)) {
+          // (a cap is odd: what it makes of a score changes sign with it)
+          if constexpr (kCap)
+            cap_scores(v, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), a.rules,
+                       [&](auto f) { tmem_map128(srow, v, f); });
           if (a.q_mode) {
 #pragma unroll
             for (int cc = 0; cc < kN; ++cc) v[cc] = a.q_mode == 1 ? -v[cc] : 0.f;
           }
           if constexpr (kCap || kBias) {
-            // (|scores| are what the loads said, also after a change of sign)
-            if constexpr (kCap)
-              cap_scores(v, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)), a.rules);
             if constexpr (kBias)
               row_add = bias_scores<kCap>(v, a.scale_log2, slope, limit - key0, ahead);
             mul = 1.f;

@@ -1015,7 +1015,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx3 *= k;
             }
           } else {
-            if constexpr (kCap) cap_scores(v, top, a.rules);
+            if constexpr (kCap)
+              cap_scores(v, top, a.rules, [&](auto f) { tmem_map128(srow, v, f); });
             if constexpr (kBias)
               row_add = bias_scores<kCap>(v, a.scale_log2, slope, limit - key0, ahead);
             mul = 1.f;

@@ -43,13 +43,15 @@ __device__ __forceinline__ float rule_rcp(float x) {
   return y;
 }
 
-// tanh x = 1 - 2 / (1 + e^2x), or the polynomial near zero, where that form
-// would cancel: relative error below 2^-20 everywhere, so a cap of any size
-// keeps the scores' own precision.
+// tanh x = 1 - 2 / (1 + e^2x): an absolute error of 1.2e-7 whatever x. A capped
+// score is off by that times the cap (0.09 under a cap of 1e6), so it is for
+// |x| > kTanhPoly, or for caps of up to 100.
 __device__ __forceinline__ float rule_tanh_far(float x) {
   return 1.f - 2.f * rule_rcp(1.f + rule_exp2(x * (2.f * kLog2e)));
 }
 
+// That, or the polynomial near zero: relative error below 2^-20 everywhere, so
+// a cap of any size keeps the scores' own precision.
 __device__ __forceinline__ float rule_tanh(float x) {
   const float u = x * x;
   const float p = fmaf(fmaf(fmaf(kTanh9, u, kTanh7), u, kTanh5), u, kTanh3);
@@ -134,19 +136,38 @@ __device__ __forceinline__ void near_pair(float s0, float s1, int cc, float scal
 }
 
 // All scores of a tile in log2 units, in place, without the bias; top: the
-// largest absolute raw score of the thread's row.
+// largest absolute raw score of the thread's row. The polynomial (in pairs on the
+// FMA pipe) where it holds for all of a warp's rows. Otherwise the exponential
+// form, alone where a cap is so small that 1.2e-7 of it is less than a score's
+// fp32 sum is off by, else with the polynomial score by score, since a tile with
+// a large score holds small ones too: each(f) puts f of the raw scores into v. Its
+// short loop keeps these two out of the unrolled code, which every tile passes:
+// 4 chunks of up to 2048 tokens over up to 8192 keys, 32/8 heads of 128, window
+// 4096, cap 50, raw scores up to 5 / 15 / 30 / 60: 190 / 258 / 252 / 364 us; all
+// unrolled 195 / 262 / 257 / 372, score by score alone 195 / 263 / 260 / 484.
+constexpr float kFarCapLog2 = 144.f;  // a cap of 100: off by at most 1.2e-5
+
+template <typename Each>
 __device__ __forceinline__ void cap_scores(float (&v)[kRuleTile], float top,
-                                           const ScoreRules &rules) {
-  if (__all_sync(0xffffffffu, top <= rules.near)) {
+                                           const ScoreRules &rules, Each each) {
+  if (__all_sync(0xffffffffu, top * rules.cap_in <= kTanhPoly)) {
 #pragma unroll
-    for (int cc = 0; cc < kRuleTile; ++cc) {
-      const float u = v[cc] * v[cc];
-      v[cc] *= fmaf(u, fmaf(u, rules.c5, rules.c3), rules.c1);
+    for (int cc = 0; cc < kRuleTile; cc += 2) {
+      const float2 x = __fmul2_rn(make_float2(v[cc], v[cc + 1]),
+                                  make_float2(rules.cap_in, rules.cap_in));
+      const float2 u = __fmul2_rn(x, x);
+      float2 p = __ffma2_rn(u, make_float2(kTanh9, kTanh9), make_float2(kTanh7, kTanh7));
+      p = __ffma2_rn(u, p, make_float2(kTanh5, kTanh5));
+      p = __ffma2_rn(u, p, make_float2(kTanh3, kTanh3));
+      p = __ffma2_rn(__fmul2_rn(x, u), p, x);
+      p = __fmul2_rn(p, make_float2(rules.cap_log2, rules.cap_log2));
+      v[cc] = p.x;
+      v[cc + 1] = p.y;
     }
+  } else if (rules.cap_log2 <= kFarCapLog2) {
+    each([&](float s) { return rules.cap_log2 * rule_tanh_far(s * rules.cap_in); });
   } else {
-#pragma unroll
-    for (int cc = 0; cc < kRuleTile; ++cc)
-      v[cc] = rules.cap_log2 * rule_tanh_far(v[cc] * rules.cap_in);
+    each([&](float s) { return rules.cap_log2 * rule_tanh(s * rules.cap_in); });
   }
 }
 

@@ -208,6 +208,26 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// v = f of each of 128 fp32 TMEM columns of this thread's lane, by way of TMEM in
+// a short loop: little code and few registers, for what runs rarely.
+template <typename F>
+__device__ __forceinline__ void tmem_map128(uint32_t taddr, float (&v)[128], F f) {
+#pragma unroll 1
+  for (int cc = 0; cc < 128; cc += 16) {
+    float w[16];
+    tmem_ld16(taddr + cc, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = f(w[i]);
+    tmem_st16(taddr + cc, w);
+  }
+  tmem_st_wait();
+#pragma unroll
+  for (int cc = 0; cc < 128; cc += 32)
+    tmem_ld32(taddr + cc, *reinterpret_cast<float(*)[32]>(&v[cc]));
+  tmem_ld_wait();
+}
+
 // TMEM allocation (one full warp executes these).
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
