@@ -1,5 +1,5 @@
 """Score rules at the ends of their ranges: scores from far below a soft cap to far past it in one
-tile, caps of any size.
+tile, caps of any size, distance slopes that are steep, zero, negative or mixed within a kv head.
 
 The tolerance follows each score's own size. A score q.k is an fp32 sum of D products, off by at
 most D 2^-23 of the sum of their magnitudes; a cap (slope at most one) adds a relative 2^-20 of the
@@ -135,3 +135,19 @@ def test_one_key_with_large_scores_among_small_ones(form, cap):
     """Its scores are large and of either sign; where they are negative, the others decide."""
     case = case_of(form, 33)
     check_ranges(Rules(case, cap=cap), spikes={0: {5: 64.0, 700: 16.0}, 1: {100: 64.0}})
+
+
+SLOPES = {"steep": [2.0, 8.0], "zero": [0.0], "negative": [-0.05], "steep negative": [-2.5],
+          "mixed": [0.0, 2.0, -0.05, 0.01], "border": [1.0285, 1.0287, -1.0287, -1.0285]}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("slopes", list(SLOPES.values()), ids=list(SLOPES))
+@pytest.mark.parametrize("rule", [{}, dict(cap=20.0), dict(window=300, prefix=[200, 40])], ids=str)
+def test_slopes_of_any_size_and_sign(form, slopes, rule):
+    """Steep ones (past what a bound of 32 columns may be off), none, ones that favour far keys."""
+    case = case_of(form, 34)
+    rules = Rules(case, alibi=True, **rule)
+    rules.slopes = np.resize(np.asarray(slopes, np.float32), case.Hq)
+    check_ranges(rules)
