@@ -377,7 +377,7 @@ def _score_mod(soft_cap, alibi_slopes, window, prefix_lens, batch: int, hq: int,
             raise ValueError("alibi_slopes must have one entry per q head")
     if prefix_lens is not None:
         pp = _ints(prefix_lens, batch, dev, "prefix_lens")
-    if window > 0x7fffffff:
+    if not -0x80000000 <= window <= 0x7fffffff:  # (ctypes would wrap it)
         raise ValueError("window must fit 32 bits")
     return PkvScoreMod(float(soft_cap), sp, int(window), pp)
 
