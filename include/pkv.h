@@ -429,7 +429,8 @@ size_t pkv_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_k
  * Hq / Hkv <= 16. workspace: device, 256-byte aligned, at least
  * pkv_tree_workspace_size(batch, Hq, Hkv, D, max_tree_tokens,
  * max_seq_len_hint) bytes, contents irrelevant on entry (two calls that can
- * overlap on the GPU need one each). max_seq_len_hint < 1: the row capacity
+ * overlap on the GPU need one each); a call that gives each query block its own
+ * CTAs, by its host-side sizes, does not look at it. max_seq_len_hint < 1: the row capacity
  * table_stride * page_size; a longer request is still computed.
  * Flagged and not computed (outputs unspecified): a request with more than
  * max_tree_tokens drafted tokens (PKV_DEVERR_TREE), a malformed qo_indptr

@@ -756,7 +756,9 @@ pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *
   const pkv::DirectPlan plan =
       pkv::tree_plan(batch, num_q_heads, g.hkv, g.d, max_tree_tokens, static_cast<int32_t>(cap),
                      d->sm_count);
-  if ((s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK) return s;
+  if (!plan.whole &&
+      (s = check_workspace(workspace, workspace_bytes, plan.workspace_bytes)) != PKV_OK)
+    return s;
   cudaError_t e = pkv::launch_tree(g, layer, q, qo_indptr, parents, o, lse, page_table,
                                    table_stride, table_idx, seq_lens, batch, total_q, num_q_heads,
                                    scale, max_tree_tokens, plan, workspace, d->err, stream);
