@@ -300,8 +300,12 @@ static pkv_status score_rules(const pkv_score_mod *mod, float scale, pkv::ScoreR
     out->c1 = static_cast<float>(c1);
     out->c3 = static_cast<float>(c1 * c * c * pkv::kTanhNear3);
     out->c5 = static_cast<float>(c1 * c * c * c * c * pkv::kTanhNear5);
-    out->near = static_cast<float>(
-        fmin(c == 0.0 ? 3e38 : pkv::kTanhNear / fabs(c), c1 == 0.0 ? 3e38 : pkv::kNearLog2 / fabs(c1)));
+    // no score is near where the coefficients leave fp32 (scales of 1e14 and more)
+    out->near =
+        !isfinite(out->c1) || !isfinite(out->c3) || !isfinite(out->c5)
+            ? -1.f
+            : static_cast<float>(fmin(c == 0.0 ? 3e38 : pkv::kTanhNear / fabs(c),
+                                      c1 == 0.0 ? 3e38 : pkv::kNearLog2 / fabs(c1)));
   }
   out->alibi_slopes = mod->alibi_slopes;
   // a window longer than any row is none (and the kernels' distances stay in 32 bits)

@@ -151,3 +151,25 @@ def test_slopes_of_any_size_and_sign(form, slopes, rule):
     rules = Rules(case, alibi=True, **rule)
     rules.slopes = np.resize(np.asarray(slopes, np.float32), case.Hq)
     check_ranges(rules)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("scale,cap", [(1e30, 1e26), (-3e37, 1e32), (1e-30, 1e-30)])
+def test_scales_at_the_ends_of_their_range_under_a_cap(form, scale, cap):
+    """A request whose q is zero scores zero: the mean of its visible values, whatever the scale."""
+    ensure_built()
+    case = case_of(form, 35)
+    rules = Rules(case, cap=cap)
+    pool, k, v, q, t = gpu_inputs(case)
+    tokens = 1 if case.kind == "decode" else int(case.qo_indptr[1])
+    q[:tokens] = 0
+    o, lse = mod_run(rules, inputs=(pool, k, v, q, t), scale=scale)
+    v, g = stored_inputs(case)[0][0][1], case.Hq // case.Hkv
+    for j in range(tokens):
+        n = rules.visible(0, j, v.shape[0]).sum()
+        want, mag = (np.repeat(x[:n].mean(0), g, 0) for x in (v, np.abs(v)))
+        sums = n * 2.0 ** -24
+        tol = (2.0 ** -8 + sums) * mag + 2.0 ** -8 * np.abs(want)
+        assert (np.abs(o[j].double().cpu().numpy() - want) <= tol).all()
+        assert (np.abs(lse[j].double().cpu().numpy() - np.log(n)) <= 2.0 ** -18 + sums).all()
