@@ -140,19 +140,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
       : "memory");
 }
 
-// One fp32 TMEM column of this thread's lane.
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  return __uint_as_float(r);
-}
-
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
-               "r"(__float_as_uint(v))
-               : "memory");
-}
-
 // tmem_ld32 that also returns the largest of the 32 values it loads
 // (tcgen05.ld.red, sm_103a): the reduction runs in the load path instead of
 // 31 max instructions on the ALU. NaN values are ignored, as by fmaxf.
@@ -300,19 +287,10 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 }
 
 // TMA tile load: the box at column x, row y of a 2-D tensor into shared
-// memory at dst (box rows of 128 bytes with the map's swizzle). Completion
-// counts the box's bytes down on `bar`.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int x, int y,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-// The same with an L2 eviction-priority policy (createpolicy): tiles that are
-// read again soon are kept (evict last), those read once go first.
+// memory at dst (box rows of 128 bytes with the map's swizzle), with an L2
+// eviction-priority policy (createpolicy): tiles that are read again soon are
+// kept (evict last), those read once go first. Completion counts the box's
+// bytes down on `bar`.
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void *tmap, int x, int y,
                                                  uint32_t bar, uint64_t policy) {
   asm volatile(
@@ -429,12 +407,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
 __device__ __forceinline__ float max3f(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
-__device__ __forceinline__ float min3f(float x, float y, float z) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 
