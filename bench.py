@@ -55,19 +55,19 @@ CSRC = os.path.join(ROOT, "paged_kv_attention_out_gb300", "csrc")
 MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
     "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
-               "sha256": "61dd1c44d2f27e6e6de49e35638038c88851931c7dc5a5017231c2ec3a3dc961",
-               "bytes": 623410752},
+               "sha256": "e17e9bb10481d0a962662b699594854878217a02ef3b0491c608f50fecd144ce",
+               "bytes": 623416819},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
     "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
                            'pkv_common.cuh'],
-               "sha256": "a8fcda746c45520e1c6368beac1fc56fb289e0f28797bb412fe52514766073b6",
-               "bytes": 492738240},
+               "sha256": "b3598c7c879daf872075357debadc17b121a21efb82907badcc121cda7d07048",
+               "bytes": 492733152},
     # cascade_prefix_kernel + decode_kernel (suffix) + decode_merge_narrow_kernel,
     # radix-shared decode through cascade decode
     "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
                             'tc_common.cuh', 'pkv_common.cuh'],
-                "sha256": "cf48a4c01fddc2cc57e0856dbf77fdbf05ecb8fdaa6b135c94e5219da14c5e83",
-                "bytes": 372185685},
+                "sha256": "4259e0145a2865e0bfb068b41e9ca1cc5c293f7293a274da60dc304bc191d6b6",
+                "bytes": 372194773},
 }
 
 

@@ -6,7 +6,7 @@
 // parents[] (a parent is an earlier token, -1 the last cached one): a row mask
 // that touches only the key tiles which hold drafted keys. The kernel is in
 // direct_tc.cuh. 16 requests with up to 32768 keys, 32/8 heads of 128, page
-// size 16: 144 us for 16 drafts each (0.95 of the copy rate), 168 for 64.
+// size 16: 144 us for 16 drafts each (0.95 of the copy rate), 169-174 for 64.
 #include "direct_tc.cuh"
 
 namespace pkv {
