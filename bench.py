@@ -55,18 +55,18 @@ CSRC = os.path.join(ROOT, "paged_kv_attention_out_gb300", "csrc")
 MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
     "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
-               "sha256": "e17e9bb10481d0a962662b699594854878217a02ef3b0491c608f50fecd144ce",
+               "sha256": "1669716ab7b83ad807ddff51e7c7bd07365e16406aac67bfa5ada04d65f24b4e",
                "bytes": 623416819},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
     "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
                            'pkv_common.cuh'],
-               "sha256": "b3598c7c879daf872075357debadc17b121a21efb82907badcc121cda7d07048",
+               "sha256": "24358ba0a2e3925448ebe1fa95cf2d679db387e1a7eeb07f7f19d776a574dd8c",
                "bytes": 492733152},
     # cascade_prefix_kernel + decode_kernel (suffix) + decode_merge_narrow_kernel,
     # radix-shared decode through cascade decode
     "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
                             'tc_common.cuh', 'pkv_common.cuh'],
-                "sha256": "4259e0145a2865e0bfb068b41e9ca1cc5c293f7293a274da60dc304bc191d6b6",
+                "sha256": "18b44097b33410e08da8d15d102e83a148b2aacca5c5058e68752dc852721fc6",
                 "bytes": 372194773},
 }
 

@@ -145,7 +145,7 @@ __device__ __forceinline__ void near_pair(float s0, float s1, int cc, float scal
 // 4 chunks of up to 2048 tokens over up to 8192 keys, 32/8 heads of 128, window
 // 4096, cap 50, raw scores up to 5 / 15 / 30 / 60: 190 / 258 / 252 / 364 us; all
 // unrolled 195 / 262 / 257 / 372, score by score alone 195 / 263 / 260 / 484.
-constexpr float kFarCapLog2 = 144.f;  // a cap of 100: off by at most 1.2e-5
+constexpr float kFarCapLog2 = 144.3f;  // caps of up to 100: off by at most 1.2e-5
 
 template <typename Each>
 __device__ __forceinline__ void cap_scores(float (&v)[kRuleTile], float top,
