@@ -43,6 +43,7 @@ struct DecodeSmem {
 struct DecodeArgs {
   static constexpr int kRules = 0;  // compile-time score rules (score_rules.cuh)
   static constexpr bool kScores = false;  // the scores are kept (decode_mass.cu)
+  static constexpr bool kTwoTerms = false;  // probabilities as two bf16 terms (split_bf16)
   const __nv_bfloat16 *pool;
   int64_t plane;
   int64_t slots;
@@ -98,6 +99,7 @@ template <int kBits>
 struct DecodeScoreArgs : DecodeRuleArgs {
   static constexpr int kRules = kBits;
   static constexpr bool kScores = true;
+  static constexpr bool kTwoTerms = true;
   float *scores;
   int64_t score_keys;
   explicit DecodeScoreArgs(const DecodeRuleArgs &a) : DecodeRuleArgs(a) {}
@@ -123,6 +125,16 @@ __device__ __forceinline__ float decode_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// p, q >= 0 as hi + rest, each a pair of bf16 (p in the lower half), to 2^-14.4 of them. hi is cut
+// off a little below them, so that rest is positive wherever they are: an infinite value of
+// V gives infinity with both (rest = 0 would give NaN).
+__device__ __forceinline__ void split_bf16(float p, float q, uint32_t &hi, uint32_t &rest) {
+  constexpr float kBelow = 1.f - 0x1p-8f;
+  const uint32_t x = __float_as_uint(p * kBelow), y = __float_as_uint(q * kBelow);
+  hi = __byte_perm(x, y, 0x7632);
+  rest = pack_bf16(p - __uint_as_float(x & 0xffff0000u), q - __uint_as_float(y & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint32_t ld_b32(const __nv_bfloat16 *p) {
@@ -401,14 +413,26 @@ __device__ __forceinline__ void decode_body(const Args &a, int hg, int split, in
       acc[mt][3] *= al1;
     }
     // P^T as the B operand (k = key, n = head): transpose the two 8x8 halves.
-    const uint32_t bp0 = movmatrix_trans(pack_bf16(p0, p1));
-    const uint32_t bp1 = movmatrix_trans(pack_bf16(p2, p3));
+    uint32_t bp0, bp1;
+    [[maybe_unused]] uint32_t rest0, rest1;  // kTwoTerms: what bp0 and bp1 leave
+    if constexpr (Args::kTwoTerms) {
+      split_bf16(p0, p1, bp0, rest0);
+      split_bf16(p2, p3, bp1, rest1);
+      rest0 = movmatrix_trans(rest0);
+      rest1 = movmatrix_trans(rest1);
+    } else {
+      bp0 = pack_bf16(p0, p1);
+      bp1 = pack_bf16(p2, p3);
+    }
+    bp0 = movmatrix_trans(bp0);
+    bp1 = movmatrix_trans(bp1);
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
       uint32_t a0, a1, a2, a3;
       ldmatrix_x4_trans(vst + swz<D>((lane & 7) + (lane >> 4) * 8, mt * 2 + ((lane >> 3) & 1)),
                         a0, a1, a2, a3);
       mma_bf16_16816(acc[mt], a0, a1, a2, a3, bp0, bp1);
+      if constexpr (Args::kTwoTerms) mma_bf16_16816(acc[mt], a0, a1, a2, a3, rest0, rest1);
     }
     __syncwarp();
   }
