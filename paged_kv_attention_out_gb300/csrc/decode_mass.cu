@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps<G>) decode_mass_kernel(const
     grid_dependency_wait();  // states and scores come from the decode kernel
     // scores and states are asked for together
     const float *sc =
-        a.scores + (static_cast<int64_t>(b) * a.hkv + h) * a.score_keys * G + k0 * G;
+        a.scores + ((static_cast<int64_t>(b) * a.hkv + h) * a.score_keys + k0) * G;
     float s[kPer][G];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
