@@ -479,8 +479,9 @@ pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *
  * scores (one for larger sizes serves smaller ones; calls that can overlap on the
  * GPU need one each). max_seq_len_hint: a bound on every seq_len (< 1: the row
  * capacity); a longer request gets its attention, its weights are left as they
- * were and PKV_DEVERR_SEQ_LEN_RANGE is flagged. A row whose every score is -inf
- * adds nothing.
+ * were and PKV_DEVERR_SEQ_LEN_RANGE is flagged. A q head whose every score is
+ * -inf adds nothing; one with a score that is NaN or +inf has NaN for its o and
+ * lse, and every key of the row gets NaN on its kv head.
  */
 size_t pkv_decode_mass_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                       int32_t head_dim, int32_t max_seq_len_hint);

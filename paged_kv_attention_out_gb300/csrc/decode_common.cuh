@@ -495,7 +495,9 @@ __device__ __forceinline__ void decode_body(const Args &a, int hg, int split, in
     O.y *= inv;
     O.z *= inv;
     O.w *= inv;
-    const float lse_nat = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    // (a sum that is NaN stays one where weights are derived from the lse)
+    const bool any = Args::kScores ? L != 0.f : L > 0.f;
+    const float lse_nat = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
     const int h = (hg * a.heads_per_cta + hs) * a.group + n;
     const int64_t bh = static_cast<int64_t>(b) * a.hq + h;
     if (final_out) {

@@ -5,6 +5,9 @@
 // and log-sum-exp of plain decode (under a soft cap, if any):
 //   mass[row, h, i] = (i < n - 1 ? mass[row, h, i] : 0) + sum over the group's q
 //   heads of exp(s_i - lse)
+// A head with a score that is NaN or +inf has a sum of NaN: it is kept through the partial
+// states and the merges (sums are compared with zero, not for being positive), so that lse, o
+// and every weight of the kv head are NaN, not only what its own split adds.
 //
 // The weights need the row's sum, which is known only when every split is done.
 // The decode kernel therefore leaves its scores (4 bytes a key and q head, where K
@@ -78,8 +81,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     float l = e;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float lse = l > 0.f ? ref + logf(l) : -INFINITY;
-    if (lane == 0) s_lse[g] = l > 0.f ? lse * kLog2e : INFINITY;
+    const float lse = l != 0.f ? ref + logf(l) : -INFINITY;
+    if (lane == 0) s_lse[g] = l != 0.f ? lse * kLog2e : INFINITY;
     if (g % static_cast<int>(gridDim.y) != split) continue;  // (a CTA of the cluster a head)
     const float *po = a.part_o + (pair0 + g) * a.pstride * D + lane * kCols;
     float v[kClusterSplits][kCols], o[kCols];
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps<G>) decode_mass_kernel(const
       for (int t = lane + 32; t < ns; t += 32) l += expf(pl[t] - ref);
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-      if (lane == 0) s_lse[warp] = l > 0.f ? (ref + logf(l)) * kLog2e : INFINITY;
+      if (lane == 0) s_lse[warp] = l != 0.f ? (ref + logf(l)) * kLog2e : INFINITY;
     }
     __syncthreads();
     float lse[G];  // +inf, no weight, for a row whose every score is -inf
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps<G>) decode_mass_kernel(const
       for (int c = 0; c < kCols; c += 2)
         *reinterpret_cast<uint32_t *>(a.o + (pair0 + warp) * D + lane * kCols + c) =
             pack_bf16(o[c] * inv, o[c + 1] * inv);
-      if (lane == 0 && a.lse) a.lse[pair0 + warp] = l > 0.f ? m + logf(l) : -INFINITY;
+      if (lane == 0 && a.lse) a.lse[pair0 + warp] = l != 0.f ? m + logf(l) : -INFINITY;
     }
     return;
   }
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps<G>) decode_mass_kernel(const
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   *reinterpret_cast<uint32_t *>(a.o + bh * D + 2 * tid) = pack_bf16(x * inv, y * inv);
-  if (tid == 0 && a.lse) a.lse[bh] = L > 0.f ? ref + logf(L) : -INFINITY;
+  if (tid == 0 && a.lse) a.lse[bh] = L != 0.f ? ref + logf(L) : -INFINITY;
 }
 
 template <int D, int G>
