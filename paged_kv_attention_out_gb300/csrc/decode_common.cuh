@@ -102,6 +102,7 @@ struct DecodeScoreArgs : DecodeRuleArgs {
   static constexpr bool kTwoTerms = true;
   float *scores;
   int64_t score_keys;
+  int32_t most_keys;  // rows with more get no weights (score_keys is rounded up)
   explicit DecodeScoreArgs(const DecodeRuleArgs &a) : DecodeRuleArgs(a) {}
   __device__ __forceinline__ void keep_scores(int b, int h, int i, int n, float s0,
                                               float s1) const {

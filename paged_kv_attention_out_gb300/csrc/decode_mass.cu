@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   const int n = a.seq_lens[b];
   const int row = a.table_idx ? a.table_idx[b] : b;
   if (row < 0 || n <= 0) return;  // (flagged above, or nothing to add)
-  if (n != ri.seq || n > mass_stride || n > a.score_keys) {
+  if (n != ri.seq || n > mass_stride || n > a.most_keys) {
     if (split == 0 && h == 0 && threadIdx.x == 0) flag_error(a.err, kErrSeqLen);
     return;
   }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps<G>) decode_mass_kernel(const
     const int ns = ri.nsplit;
     const int n = a.seq_lens[b];
     const int row = a.table_idx ? a.table_idx[b] : b;
-    const bool fits = row >= 0 && n >= 0 && n == ri.seq && n <= f.mass_stride && n <= a.score_keys;
+    const bool fits = row >= 0 && n >= 0 && n == ri.seq && n <= f.mass_stride && n <= a.most_keys;
     const int k0 = chunk * kFinishKeys;
     if (!fits && row >= 0 && n > 0 && chunk == 0 && h == 0 && tid == 0)
       flag_error(a.err, kErrSeqLen);
@@ -373,6 +373,7 @@ DecodeMassLayout decode_mass_layout(int32_t batch, int32_t hq, int32_t hkv, int3
                                     int32_t max_keys, int32_t sm_count) {
   DecodeMassLayout l{};
   l.plan = plan_decode_rules(batch, hq, hkv, d, max_keys, sm_count);
+  l.most_keys = max_keys;
   l.score_keys = (static_cast<int64_t>(max_keys) + 15) & ~int64_t(15);
   const size_t states =
       static_cast<size_t>(decode_rules_states(batch, hq, hkv, max_keys, sm_count));
@@ -427,6 +428,7 @@ cudaError_t launch_decode_mass(const PoolGeom &g, int32_t layer, const void *q, 
   auto main = [&](auto args) {
     args.scores = scores;
     args.score_keys = lay.score_keys;
+    args.most_keys = lay.most_keys;
     if (cluster)
       return g.d == 128 ? launch_cluster<128>(args, mass, mass_stride, grid, stream)
                         : launch_cluster<64>(args, mass, mass_stride, grid, stream);
@@ -440,6 +442,7 @@ cudaError_t launch_decode_mass(const PoolGeom &g, int32_t layer, const void *q, 
                lay.plan.splits > kFewStates ? base.group : 0};
   f.d.scores = scores;
   f.d.score_keys = lay.score_keys;
+  f.d.most_keys = lay.most_keys;
   const dim3 fgrid(
       f.merge_ctas + static_cast<unsigned>((lay.score_keys + kFinishKeys - 1) / kFinishKeys),
       g.hkv, batch);

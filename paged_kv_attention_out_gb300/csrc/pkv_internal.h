@@ -306,7 +306,8 @@ cudaError_t launch_extend_mass(const PoolGeom &g, const MassArgs &a, const void 
 // fp32, keys the hint rounded up to 16).
 struct DecodeMassLayout {
   DecodePlan plan;
-  int64_t score_keys;
+  int32_t most_keys;   // the hint
+  int64_t score_keys;  // a row's room for scores
   size_t lse_offset;
   size_t score_offset;
   size_t total_bytes;
