@@ -477,10 +477,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     auto there = [&](int it) { return s_item[it % kItemSlots].n > 0; };
     if ((size == 1 || n_items > 0) && (ok = wait_item(0)) && there(0))
       copy_keys(s_item[0], look(s_item[0]));
-    // over all items: query tiles and units before this one, and the first unit of this
-    // group in it
+    // over all items: query tiles and units before this one
     uint32_t tiles = 0, units = 0;
-    int next = group;
     for (int it = 0; size == 1 || it < n_items; ++it) {
       const int islot = it % kItemSlots;
       float had = 0.f;
@@ -494,8 +492,10 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                        m.key0 + own);
         float sum0 = 0.f, sum1 = 0.f;  // of this thread's key in both key tiles
         const int n_units = 2 * m.mine - m.one;
+        // (from the first group on in every item, so that a sum does not depend on the items
+        // that this CTA had before; the groups have just met, so none has to wait for it)
 #pragma unroll 1
-        for (; next < n_units; next += kGroups) {
+        for (int next = group; next < n_units; next += kGroups) {
           const int v = next - m.one;
           const int i = v < 0 ? next : m.one + (v >> 1);
           const int kt = v < 0 ? 0 : v & 1;
@@ -525,7 +525,6 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             }
           }
         }
-        next -= n_units;
         tiles += static_cast<uint32_t>(m.mine);
         units += static_cast<uint32_t>(n_units);
         float *sums = reinterpret_cast<float *>(smem + S::kSum) +
