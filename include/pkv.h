@@ -554,7 +554,9 @@ pkv_status pkv_kv_evict(const pkv_pool *pool, int32_t layer, float *key_mass, in
  *   angle = new_pos * new_freq[m] - old_pos * old_freq[m]
  *   (a, b) = factor * (a cos - b sin, b cos + a sin)
  * with pairs as in pkv_norm_rope_kv_store (halves, or neighbours if interleaved;
- * dims from rot_dim on unchanged), fp32 from exact angles, rounded once.
+ * dims from rot_dim on unchanged), in fp32 from exact angles, rounded once: off
+ * by 2^-21.2 of the pair's radius before that, 2^-19.3 if position_heads > 1
+ * (and at positions near 2^31 by the angle's own 2^-22 of a turn).
  * old_freq, new_freq: device fp32 [rot_dim / 2], radians per position (finite);
  * one of them may be NULL: not rotated before, or after. old_positions,
  * new_positions: device int32 [batch, position_heads, position_stride], entry i

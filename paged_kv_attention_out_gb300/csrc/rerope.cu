@@ -8,18 +8,25 @@
 // in fp32, rounded once to bf16. Angles are exact before their sine: a frequency
 // is kept as a 64-bit binary fraction of a turn, so position times frequency is an
 // integer product modulo 2^64 and whole turns drop out by themselves. The fraction
-// is off by 2^-54 of its value (a product in 64 bits and the rounding), a position
-// of 2^31 radians by 2^-22 of a turn; an fp32 product would be off by 2^-24 of
-// the angle, 0.008 radians at 131072. Within half a turn the hardware's sine and cosine
-// are off by 2^-21.2 at most (CUDA's stated bound), 2^-8 of a bf16 step.
+// is off by 2^-52 of its value (1 / (2 pi) and the product, rounded in 64 bits) and by 2^-64, a
+// position of 2^31 radians by 2^-23 of a turn; an fp32 product would be off by 2^-24 of
+// the angle, 0.008 radians at 131072.
+//
+// Sines and cosines: polynomials, off by 2^-23.2 at most, so that a turned value is off by
+// 2^-21.2 of its pair's radius before it is rounded. Where positions differ by kv head, angles
+// are computed for every head and bound the call: there they come from the hardware,
+// off by up to 2^-21.2 on [-pi, pi] (CUDA's stated bound), a turned value by 2^-19.3 of
+// the radius, where half a step of bf16 is 2^-9 of the value or more. 8 rows of up to 16000
+// keys, 8 heads of 128: 62.8 us, with the polynomials 68.1; one position a key, 8 rows of up
+// to 32768: 84.4 us with either.
 //
 // Bound by memory: the rotated part of every key is read and written once, and
 // nothing is read for the angles but the positions. rot_dim / 16 lanes hold a
 // key's pairs, both chunks of 16 bytes of the same pairs, compute their eight
 // angles once and use them for every kv head (once a head where positions differ
-// by head). Pairs whose angle is zero under a factor of one are neither read nor
-// written. Measured: 8 rows of up to 32768 keys, 8 heads of 128, 84 us (0.90 of the copy
-// rate).
+// by head). A lane writes nothing where none of its eight pairs turns under a factor of
+// one; its first heads are read all the same, since they come while the angles are computed.
+// Measured: 8 rows of up to 32768 keys, 8 heads of 128, 84 us (0.90 of the copy rate).
 #include "bf16x8.cuh"
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
@@ -51,6 +58,24 @@ __device__ __forceinline__ uint4 load_here(const uint4 *p) {
 
 // Of 2^-32 turns.
 constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
+
+// Sine and cosine of t / 2^32 turns, off by 2^-23.2 at most: polynomials (least maximum error,
+// by reweighted least squares) in w quarter turns, |w| <= 1/2, round the nearest quarter.
+__device__ __forceinline__ void sin_cos_turn(uint32_t t, float *sn, float *cs) {
+  const uint32_t quarter = (t + 0x20000000u) >> 30;
+  const float w = static_cast<float>(static_cast<int32_t>(t << 2)) * 0x1p-32f;
+  const float z = w * w;
+  float s = fmaf(z, -0.0046021771f, 0.079680227f);
+  s = fmaf(z, s, -0.64596349f);
+  s = w * fmaf(z, s, 1.5707964f);
+  float c = fmaf(z, 0.00091181189f, -0.020863504f);
+  c = fmaf(z, c, 0.25366962f);
+  c = fmaf(z, c, -1.2337005f);
+  c = fmaf(z, c, 1.f);
+  const bool odd = quarter & 1;
+  *sn = __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 2) << 30);
+  *cs = __uint_as_float(__float_as_uint(odd ? s : c) ^ (quarter + 1 & 2) << 30);
+}
 
 struct Turns {
   float cs[8], sn[8];
@@ -122,10 +147,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rerope_kernel(const RopeArgs 
                                    : static_cast<uint64_t>(new_pos) * s_new[m] -
                                          static_cast<uint64_t>(old_pos) * s_old[m];
         t.any = t.any || turn != 0;
-        // radians in [-pi, pi)
-        const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * kRadians;
-        t.sn[e] = __sinf(x) * a.factor;
-        t.cs[e] = __cosf(x) * a.factor;
+        const uint32_t part = static_cast<uint32_t>(turn >> 32);
+        float sn, cs;
+        if constexpr (kByHead) {
+          const float x = static_cast<float>(static_cast<int32_t>(part)) * kRadians;  // [-pi, pi)
+          sn = __sinf(x);
+          cs = __cosf(x);
+        } else {
+          sin_cos_turn(part, &sn, &cs);
+        }
+        t.sn[e] = sn * a.factor;
+        t.cs[e] = cs * a.factor;
       }
       return t;
     };
