@@ -55,8 +55,8 @@ CSRC = os.path.join(ROOT, "paged_kv_attention_out_gb300", "csrc")
 MEASURED_TRAFFIC = {
     # decode_kernel + decode_merge_kernel, Llama-3-8B-shaped decode
     "decode": {"sources": ['decode.cu', 'decode_common.cuh', 'score_rules.cuh', 'pkv_common.cuh'],
-               "sha256": "ffb5963ff8c825cc31872601c0850ad67ba3b4239a79afc0bdc03bf83db4857b",
-               "bytes": 624006485},
+               "sha256": "26fb4ab9cbabac67cfc2e857b99d3322a8ff87d3f6d19ce3bfaf85042715f94d",
+               "bytes": 623983531},
     # extend_gather_kernel + extend_tc_persistent_kernel, chunked-prefill extend
     "extend": {"sources": ['extend.cu', 'score_rules.cuh', 'tensor_map.cu', 'tc_common.cuh',
                            'pkv_common.cuh'],
@@ -66,8 +66,8 @@ MEASURED_TRAFFIC = {
     # radix-shared decode through cascade decode
     "cascade": {"sources": ['cascade.cu', 'decode.cu', 'decode_common.cuh', 'score_rules.cuh',
                             'tc_common.cuh', 'pkv_common.cuh'],
-                "sha256": "8eadbe480354d934c0e2c109ed6c5625e377504f358e3c4a9a158645e5d5f053",
-                "bytes": 372281344},
+                "sha256": "b7a95376527e789cdb72acbae2386548278b7fd12aac9af8e5b6c568f9c9e6df",
+                "bytes": 372301472},
 }
 
 

@@ -624,7 +624,8 @@ def _mass_arg(key_mass, page_table, table_idx, batch: int, hkv: int, dev: int):
     if h != hkv:
         raise ValueError("key_mass must have the pool's kv heads")
     if rows < (batch if table_idx is None else page_table.shape[0]):
-        raise ValueError("key_mass must have a row per request, or per page_table row with table_idx")
+        raise ValueError("key_mass must have a row per request, or per page_table row with "
+                         "table_idx")
     return p, stride
 
 

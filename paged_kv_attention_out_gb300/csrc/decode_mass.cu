@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   for (int i = begin + static_cast<int>(threadIdx.x); i < end; i += kDecodeThreads) {
     float sum = i < n - 1 ? __ldcg(mass + i) : 0.f;
     for (int g = 0; g < a.group; ++g)
-      if (s_lse[g] != INFINITY) sum += decode_exp2(sc[static_cast<int64_t>(i) * a.group + g] - s_lse[g]);
+      if (s_lse[g] != INFINITY)
+        sum += decode_exp2(sc[static_cast<int64_t>(i) * a.group + g] - s_lse[g]);
     mass[i] = sum;
   }
 }
@@ -379,8 +380,8 @@ DecodeMassLayout decode_mass_layout(int32_t batch, int32_t hq, int32_t hkv, int3
       static_cast<size_t>(decode_rules_states(batch, hq, hkv, max_keys, sm_count));
   l.lse_offset = (states * d * sizeof(float) + 255) & ~size_t(255);
   l.score_offset = l.lse_offset + ((states * sizeof(float) + 255) & ~size_t(255));
-  l.total_bytes = l.score_offset +
-                  static_cast<size_t>(batch) * hq * static_cast<size_t>(l.score_keys) * sizeof(float);
+  const size_t scores = static_cast<size_t>(batch) * hq * static_cast<size_t>(l.score_keys);
+  l.total_bytes = l.score_offset + scores * sizeof(float);
   return l;
 }
 

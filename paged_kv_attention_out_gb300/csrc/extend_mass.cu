@@ -65,7 +65,7 @@ constexpr int kMassThreads = (kSumWarps + 2) * 32;
 constexpr int kCopyWarps = 8;  // of the sum warps, that load K
 constexpr int kBufs = 4;       // score buffers
 constexpr int kTmemCols = kBufs * kM;
-constexpr int kStages = 4;     // query tiles in shared memory (their extra k-steps fill a row of 128 bytes)
+constexpr int kStages = 4;     // query tiles in shared memory (their extra k-steps fill 128 bytes)
 constexpr int kLseSlots = 8;   // query tiles whose lse is in shared memory
 constexpr int kItemSlots = 8;  // items planned ahead
 constexpr int kMaxMassCluster = 8;
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, x);
     if (lane == 0 && mine > 0)
-      atomicAdd(reinterpret_cast<unsigned long long *>(&s_total), static_cast<unsigned long long>(mine));
+      atomicAdd(reinterpret_cast<unsigned long long *>(&s_total),
+                static_cast<unsigned long long>(mine));
   }
   // A cluster's items are `cluster`, `cluster` + clusters, .. (one, where the grid was
   // sized right). A CTA on its own takes over further ones from CTAs that have not
@@ -778,7 +779,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
               const float left = __hisinf(x0) ? 0.f : x - __bfloat162float(x0);
               const __nv_bfloat16 x1 = __float2bfloat16_rn(left);
               const __nv_bfloat16 x2 = __float2bfloat16_rn(left - __bfloat162float(x1));
-              *reinterpret_cast<uint2 *>(smem + S::kFold + sw128_offset(kM, 4 * lane + e, 16 * st)) =
+              const uint32_t at = sw128_offset(kM, 4 * lane + e, 16 * st);
+              *reinterpret_cast<uint2 *>(smem + S::kFold + at) =
                   make_uint2(__bfloat16_as_ushort(x0) |
                                  static_cast<uint32_t>(__bfloat16_as_ushort(x1)) << 16,
                              __bfloat16_as_ushort(x2));
@@ -1122,7 +1124,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const uint64_t dq = dq0 + static_cast<uint64_t>((q * S::kTileBytes) >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16_ss(tmem + buf * kM, dk + kstep(ks), dq + kstep(ks), idesc, ks > 0 ? 1u : 0u);
+              umma_bf16_ss(tmem + buf * kM, dk + kstep(ks), dq + kstep(ks), idesc,
+                           ks > 0 ? 1u : 0u);
             umma_commit(bar(kFewSFull + buf));
           }
           __syncwarp();

@@ -1,14 +1,16 @@
-"""The output of decode with weights (pkv_paged_decode_attn_mass) to the precision of its own rounding: the
-probabilities enter the product with the values to more bits than bf16 has.
+"""The output of decode with weights (pkv_paged_decode_attn_mass) to the precision of its own
+rounding: the probabilities enter the product with the values to more bits than bf16 has.
 
-Inputs for which nothing else rounds: q and keys of -1, 0, 1, so that raw scores are exact, values of -1
-and 1. Tolerance, with sum p |v| / sum p = 1: a probability is the sum of two bf16 terms, the second between 2^-8
-and 2^-6.4 of it and rounded by at most 2^-8 of itself: 2^-14.4. A score in log2 units is at most 64 / 16 log2(e) = 5.8
-in magnitude, rounded twice (2^-24 of it each) and less the maximum once more (2^-24 of 11.6): 2^-20 in all;
-exp2 adds 2^-22 of its value; numerator and normaliser are off by as much, together below 2^-18. Fp32 sums: at
-most 64 sequential steps, each within a product of 16 terms or of a merge, at 2^-23: 2^-17. In all below 2^-14; then half a
-step of the bf16 result, 2^-8 of it at most. The signs of the values alternate with the size of the
-probabilities, so that results are small beside the 2^-8 that probabilities rounded to bf16 are off by."""
+Inputs for which nothing else rounds: q and keys of -1, 0, 1, so that raw scores are exact,
+values of -1 and 1. Tolerance, with sum p |v| / sum p = 1: a probability is the sum of two bf16
+terms, the second between 2^-8 and 2^-6.4 of it and rounded by at most 2^-8 of itself: 2^-14.4. A
+score in log2 units is at most 64 / 16 log2(e) = 5.8 in magnitude, rounded twice (2^-24 of it
+each) and less the maximum once more (2^-24 of 11.6): 2^-20 in all; exp2 adds 2^-22 of its value;
+numerator and normaliser are off by as much, together below 2^-18. Fp32 sums: at most 64
+sequential steps, each within a product of 16 terms or of a merge, at 2^-23: 2^-17. In all below
+2^-14; then half a step of the bf16 result, 2^-8 of it at most. The signs of the values alternate
+with the size of the probabilities, so that results are small beside the 2^-8 that probabilities
+rounded to bf16 are off by."""
 from __future__ import annotations
 
 import numpy as np
@@ -21,8 +23,8 @@ BEFORE_ROUNDING, OUT_ROUNDING = 2.0 ** -14, 2.0 ** -8
 
 
 def make(n, hq, hkv, d, seed):
-    """q [hq, d], keys and values [n, hkv, d] in 64 bits; values of dim x alternate by the probability of
-    q head x % group."""
+    """q [hq, d], keys and values [n, hkv, d] in 64 bits; values of dim x alternate by the
+    probability of q head x % group."""
     g = np.random.default_rng(seed)
     q = g.integers(-1, 2, (hq, d)).astype(np.float64)
     k = g.integers(-1, 2, (n, hkv, d)).astype(np.float64)
@@ -93,7 +95,8 @@ def test_infinite_values_stay_infinite():
                      device="cuda")
     pkv.pkv_paged_decode_attn_mass(pool.cuda(), 0, q, o, lse, torch.zeros(1, 2, 300, device="cuda"),
                                    torch.arange(300, dtype=torch.int32, device="cuda")[None],
-                                   torch.tensor([300], dtype=torch.int32, device="cuda"), 1 / 16, 300, ws)
+                                   torch.tensor([300], dtype=torch.int32, device="cuda"), 1 / 16,
+                                   300, ws)
     o = o[0].cpu()
     assert torch.isfinite(lse).all()
     hit = {i % 64 for i in range(0, 300, 7)}

@@ -1,4 +1,5 @@
-"""Offsets past 32 bits into the scores that decode with weights (pkv_paged_decode_attn_mass) keeps in its workspace."""
+"""Offsets past 32 bits into the scores that decode with weights (pkv_paged_decode_attn_mass) keeps
+in its workspace."""
 from __future__ import annotations
 
 import math
@@ -15,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 
 def test_scores_of_a_batch_past_32_bits():
-    """2.7e9 scores in the workspace: the last request has the bits of the first, whose pages and q it shares."""
+    """2.7e9 scores in the workspace: the last request has the bits of the first, whose pages and q
+    it shares."""
     lens = [300, 5, 77, 260] * 10
     lens[-1] = lens[0]
     case = W.random_case(11, seq_lens=lens, Hq=32, Hkv=8, D=64, P=16)
@@ -32,8 +34,8 @@ def test_scores_of_a_batch_past_32_bits():
     o, lse = nan_outputs(q)
     wide = torch.zeros(case.B, hint // 16 + 1, dtype=torch.int32, device="cuda")
     wide[:, :t["page_table"].shape[1]] = t["page_table"]
-    pkv.pkv_paged_decode_attn_mass(pool, case.layer, q, o, lse, mass, wide, t["seq_lens"], case.scale, hint,
-                                   ws)
+    pkv.pkv_paged_decode_attn_mass(pool, case.layer, q, o, lse, mass, wide, t["seq_lens"], case.scale,
+                                   hint, ws)
     assert pkv.pkv_read_device_errors() == 0
     for x in (o, lse, mass):
         assert torch.equal(x[0], x[-1])
@@ -45,8 +47,8 @@ def test_scores_of_a_batch_past_32_bits():
 
 
 def test_scores_of_a_row_past_32_bits():
-    """A row of more than 2^28 keys and eight q heads: 2^31 scores and more. Every table entry is the same page, so
-    weights repeat with its size."""
+    """A row of more than 2^28 keys and eight q heads: 2^31 scores and more. Every table entry is
+    the same page, so weights repeat with its size."""
     ensure_built()
     import paged_kv_attention_out_gb300 as pkv
     page, n, hq, d = 65536, 2 ** 28 + 5000, 8, 64
@@ -56,9 +58,11 @@ def test_scores_of_a_row_past_32_bits():
     table = torch.zeros(1, -(-n // page), dtype=torch.int32, device="cuda")
     o, lse = nan_outputs(q)
     mass = torch.zeros(1, 1, n + 3, device="cuda")
-    ws = torch.empty(pkv.pkv_decode_mass_workspace_size(1, hq, 1, d, n), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pkv.pkv_decode_mass_workspace_size(1, hq, 1, d, n), dtype=torch.uint8,
+                     device="cuda")
     pkv.pkv_paged_decode_attn_mass(pool, 0, q, o, lse, mass, table,
-                                   torch.tensor([n], dtype=torch.int32, device="cuda"), d ** -0.5, n, ws)
+                                   torch.tensor([n], dtype=torch.int32, device="cuda"), d ** -0.5, n,
+                                   ws)
     assert pkv.pkv_read_device_errors() == 0
     s = (q[0].double() @ pool[0, 0, 0, :, 0].double().T) * d ** -0.5  # [hq, page]
     e, v = s.exp(), pool[1, 0, 0, :, 0].double()
@@ -68,13 +72,15 @@ def test_scores_of_a_row_past_32_bits():
     want_o = (full * (e @ v) + e[:, :rest] @ v[:rest]) / total[:, None]
     mag = (full * (e @ v.abs()) + e[:, :rest] @ v[:rest].abs()) / total[:, None]
     # (bf16 probabilities would be allowed as well)
-    assert ((o[0].double() - want_o).abs() <= (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * want_o.abs()).all()
-    # a weight is off by its score's and the lse's error (mass_reference), the lse also by fp32 sums of at most
-    # 2^11 sequential terms a warp and of 2^12 states: 2^-12 each at worst
+    tol = (2 ** -8 + 2 ** -10) * mag + 2 ** -8 * want_o.abs()
+    assert ((o[0].double() - want_o).abs() <= tol).all()
+    # a weight is off by its score's and the lse's error (mass_reference), the lse also by fp32 sums
+    # of at most 2^11 sequential terms a warp and of 2^12 states: 2^-12 each at worst
     want = (e / total[:, None]).sum(0)
     got = mass[0, 0, :full * page].view(full, page)
     for at in range(0, full, 256):
         assert ((got[at:at + 256].double() - want).abs() <= 2 ** -10 * want).all(), at
-    assert ((mass[0, 0, full * page:n].double() - want[:rest]).abs() <= 2 ** -10 * want[:rest]).all()
+    last = mass[0, 0, full * page:n].double()
+    assert ((last - want[:rest]).abs() <= 2 ** -10 * want[:rest]).all()
     assert (mass[0, 0, n:] == 0).all()
     assert math.isclose(float(mass.double().sum()), hq, rel_tol=2 ** -10)

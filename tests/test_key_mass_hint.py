@@ -1,4 +1,5 @@
-"""The hint of decode with weights (pkv_paged_decode_attn_mass) bounds the rows whose weights are added to the key."""
+"""The hint of decode with weights (pkv_paged_decode_attn_mass) bounds the rows whose weights are
+added to the key."""
 from __future__ import annotations
 
 import pytest
@@ -10,8 +11,8 @@ from paged_kv_attention_out_gb300 import workloads as W
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("lens,hint", [([105, 100, 90], 100), ([17, 16, 15], 15), ([1009, 1008, 1007], 1007),
-                                       ([2, 1], 1)])
+@pytest.mark.parametrize("lens,hint", [([105, 100, 90], 100), ([17, 16, 15], 15),
+                                       ([1009, 1008, 1007], 1007), ([2, 1], 1)])
 def test_rows_just_past_the_hint_are_flagged(lens, hint):
     """A hint is a bound to the key, in one launch and in two."""
     for copies in (1, 60):

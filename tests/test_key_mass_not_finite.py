@@ -1,5 +1,6 @@
-"""Scores that are NaN or infinite in decode with weights (pkv_paged_decode_attn_mass): a q head with a score that
-is NaN or +inf has NaN for its lse and its output and gives NaN to every key of the row; -inf is no weight."""
+"""Scores that are NaN or infinite in decode with weights (pkv_paged_decode_attn_mass): a q head
+with a score that is NaN or +inf has NaN for its lse and its output and gives NaN to every key of
+the row; -inf is no weight."""
 from __future__ import annotations
 
 import numpy as np
@@ -21,7 +22,8 @@ def run(lens, hq=8, hkv=2, d=64, change=lambda k, q: None, cap=0.0):
     k = torch.randn(B, most, hkv, d, generator=g).bfloat16()
     q = torch.randn(B, hq, d, generator=g).bfloat16()
     change(k, q)
-    pool = torch.stack([k, torch.randn(k.shape, generator=g).bfloat16()]).view(2, 1, B * most, 1, hkv, d)
+    v = torch.randn(k.shape, generator=g).bfloat16()
+    pool = torch.stack([k, v]).view(2, 1, B * most, 1, hkv, d)
     table = torch.arange(B * most, dtype=torch.int32).view(B, most).cuda()
     mass = torch.rand(B, hkv, most + 5, generator=g).cuda()
     before = mass.clone()
@@ -30,8 +32,8 @@ def run(lens, hq=8, hkv=2, d=64, change=lambda k, q: None, cap=0.0):
     ws = torch.empty(pkv.pkv_decode_mass_workspace_size(B, hq, hkv, d, most), dtype=torch.uint8,
                      device="cuda")
     pkv.pkv_paged_decode_attn_mass(pool.cuda(), 0, q.cuda(), o, lse, mass, table,
-                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), d ** -0.5, most,
-                                   ws, soft_cap=cap)
+                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), d ** -0.5,
+                                   most, ws, soft_cap=cap)
     assert pkv.pkv_read_device_errors() == 0
     return o.cpu(), lse.cpu(), mass.cpu(), before.cpu(), k.double().numpy(), q.double().numpy()
 

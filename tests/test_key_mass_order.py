@@ -1,5 +1,5 @@
-"""The weights of a chunk (pkv_paged_extend_mass) are added in an order that does not depend on which CTA
-came to an item when: the same bits from every call, alone or beside other work."""
+"""The weights of a chunk (pkv_paged_extend_mass) are added in an order that does not depend on
+which CTA came to an item when: the same bits from every call, alone or beside other work."""
 from __future__ import annotations
 
 import pytest

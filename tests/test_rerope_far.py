@@ -1,10 +1,12 @@
-"""Re-rotation (pkv_kv_rerope) at positions over the whole of 32 bits, against angles reduced in exact arithmetic.
+"""Re-rotation (pkv_kv_rerope) at positions over the whole of 32 bits, against angles reduced in
+exact arithmetic.
 
-Tolerance: that of test_rerope, and what its angles are off by at such positions. A frequency is kept as a fraction of a
-turn, off by 2^-52 of its value (the rounded 1 / (2 pi) and a product in 64 bits) and by 2^-64 (cut off): with frequencies of
-up to 1 radian and positions, or a distance, of up to 2^32, by 2^32 (2^-52 / (2 pi) + 2^-64) turns for the
-one product and as much for the other: 2^-18.99 radians together, which move each of the pair's two products by that
-much of |a| or |b|: 2^-18.49 of its radius."""
+Tolerance: that of test_rerope, and what its angles are off by at such positions. A frequency is
+kept as a fraction of a turn, off by 2^-52 of its value (the rounded 1 / (2 pi) and a product in
+64 bits) and by 2^-64 (cut off): with frequencies of up to 1 radian and positions, or a distance,
+of up to 2^32, by 2^32 (2^-52 / (2 pi) + 2^-64) turns for the one product and as much for the
+other: 2^-18.99 radians together, which move each of the pair's two products by that much of |a|
+or |b|: 2^-18.49 of its radius."""
 from __future__ import annotations
 
 from decimal import Decimal, getcontext
@@ -66,7 +68,8 @@ def test_whole_range_of_positions(same, sides, interleaved):
     n, rot, hkv = 90, 64, 2
     g = torch.Generator().manual_seed(5)
     old, new = (torch.randint(LOW, HIGH + 1, (1, hkv, n), generator=g) for _ in range(2))
-    for i, (a, b) in enumerate([(LOW, HIGH), (HIGH, LOW), (LOW, LOW), (HIGH, HIGH), (0, LOW), (HIGH, 0), (-1, HIGH)]):
+    for i, (a, b) in enumerate([(LOW, HIGH), (HIGH, LOW), (LOW, LOW), (HIGH, HIGH), (0, LOW),
+                                (HIGH, 0), (-1, HIGH)]):
         old[0, :, i], new[0, :, i] = a, b
     pool, table = make([n], hkv=hkv, d=128)
     before = pool.cpu()
@@ -74,9 +77,11 @@ def test_whole_range_of_positions(same, sides, interleaved):
     fn = fo if same else freqs(rot, 40000.0)
     i = torch.arange(n).expand(1, hkv, n)
     pkv.pkv_read_device_errors()
-    pkv.pkv_kv_rerope(pool, 1, table, torch.tensor([n], dtype=torch.int32, device="cuda"), fo.cuda(), fn.cuda(),
+    pkv.pkv_kv_rerope(pool, 1, table, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                      fo.cuda(), fn.cuda(),
                       old_positions=old.int().cuda() if sides != "new" else None,
-                      new_positions=new.int().cuda() if sides != "old" else None, interleaved=interleaved)
+                      new_positions=new.int().cuda() if sides != "old" else None,
+                      interleaved=interleaved)
     assert pkv.pkv_read_device_errors() == 0
     old, new = (i if sides == "new" else old), (i if sides == "old" else new)
     slots = (table[0].cpu().long()[:, None] * 16 + torch.arange(16)).reshape(-1)[:n]

@@ -1,10 +1,13 @@
-"""Re-rotation (pkv_kv_rerope) where the two products of a pair cancel, so that bf16 rounding hides nothing.
+"""Re-rotation (pkv_kv_rerope) where the two products of a pair cancel, so that bf16 rounding hides
+nothing.
 
-Tolerance: sine and cosine are off by 2^-23.2 at most, the angle (cut to 2^-32 of a turn, from a fraction kept to
-2^-52 of a frequency and 2^-64) by 2^-28, so the turned value by 2^0.5 (2^-23.2 + 2^-28) of the pair's radius R; the product
-with the factor, the products with a and b and their sum add 4 x 2^-24 R: 2^-21.28 R in all. Where positions differ by kv head the hardware's sine and
-cosine are used, with the bound of test_rerope. Then half a bf16 step of the value, 2^-8 of it at most. a and b
-are the bf16 numbers, of 2^14 pairs, that bring the value nearest to zero: below 2^-13 R mostly."""
+Tolerance: sine and cosine are off by 2^-23.2 at most, the angle (cut to 2^-32 of a turn, from a
+fraction kept to 2^-52 of a frequency and 2^-64) by 2^-28, so the turned value by 2^0.5 (2^-23.2 +
+2^-28) of the pair's radius R; the product with the factor, the products with a and b and their sum
+add 4 x 2^-24 R: 2^-21.28 R in all. Where positions differ by kv head the hardware's sine and cosine
+are used, with the bound of test_rerope. Then half a bf16 step of the value, 2^-8 of it at most. a
+and b are the bf16 numbers, of 2^14 pairs, that bring the value nearest to zero: below 2^-13 R
+mostly."""
 from __future__ import annotations
 
 import numpy as np
@@ -49,12 +52,14 @@ def test_values_that_cancel(interleaved, by_head):
     keys = x.reshape(n, hkv, rot) if interleaved else x.transpose(0, 1, 3, 2).reshape(n, hkv, rot)
     pool[0, 1].view(-1, hkv, 128)[slots.cuda()] = torch.tensor(keys).bfloat16().cuda()
     assert np.median(np.abs(want[..., 0]) / radius) < 2.0 ** -13
-    pkv.pkv_kv_rerope(pool, 1, table, torch.tensor([n], dtype=torch.int32, device="cuda"), None, f.cuda(),
-                      new_positions=torch.tensor(pos, dtype=torch.int32, device="cuda"),
+    pkv.pkv_kv_rerope(pool, 1, table, torch.tensor([n], dtype=torch.int32, device="cuda"), None,
+                      f.cuda(), new_positions=torch.tensor(pos, dtype=torch.int32, device="cuda"),
                       interleaved=interleaved)
     assert pkv.pkv_read_device_errors() == 0
     got = pool[0, 1].view(-1, hkv, 128)[slots.cuda()].double().cpu().numpy()
-    got = got.reshape(n, hkv, -1, 2) if interleaved else got.reshape(n, hkv, 2, -1).transpose(0, 1, 3, 2)
+    got = (got.reshape(n, hkv, -1, 2) if interleaved else
+           got.reshape(n, hkv, 2, -1).transpose(0, 1, 3, 2))
     off = np.abs(got - want) - HALF_BF16 * np.abs(want)
     worst = (off / radius[..., None]).max()
-    assert worst <= (FP32_PART if by_head else ONE_POSITION), f"off by 2^{np.log2(worst):.2f} of the pair's radius"
+    assert worst <= (FP32_PART if by_head else ONE_POSITION), \
+        f"off by 2^{np.log2(worst):.2f} of the pair's radius"
