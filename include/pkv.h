@@ -461,9 +461,10 @@ pkv_status pkv_paged_tree_attn(const pkv_pool *pool, int32_t layer, const void *
  * over queries and over the Hq / Hkv q heads of the group. One buffer per layer;
  * two requests of a call may not share a row. A request with more than
  * mass_stride keys (or 2^30, in any of these calls) is flagged
- * (PKV_DEVERR_SEQ_LEN_RANGE) and its weights are left as they were. An eviction keeps different keys for each kv head, so afterwards
- * a key's index is its place, not its position: calls whose rules go by distance
- * (alibi_slopes, window) are no longer meaningful for the row, soft caps are.
+ * (PKV_DEVERR_SEQ_LEN_RANGE) and its weights are left as they were. An eviction
+ * keeps different keys for each kv head, so afterwards a key's index is its place,
+ * not its position: calls whose rules go by distance (alibi_slopes, window) are no
+ * longer meaningful for the row, soft caps are.
  */
 
 /*
@@ -506,10 +507,11 @@ pkv_status pkv_paged_decode_attn_mass(const pkv_pool *pool, int32_t layer, const
  * keys, whose entries need not be set, start here, and with accumulate = 0 the
  * prefix's do too. Queries whose lse is -inf give nothing; a score that is NaN
  * gives NaN to its key, an lse that is to every key that its query sees. A request
- * without queries is left as it was. Hq / Hkv <= 16. The hints bound the seq_lens and their sum as in extend (< 1: the row
- * capacity; batch x max_seq_len_hint); they size the launch only. num_last also
- * says how many queries of a request count at most: many short chunks over long
- * rows are faster with num_last = the longest chunk than with 0. Flagged and left as they were: a request with a malformed
+ * without queries is left as it was. Hq / Hkv <= 16. The hints bound the seq_lens
+ * and their sum as in extend (< 1: the row capacity; batch x max_seq_len_hint);
+ * they size the launch only. num_last also bounds the queries of a request that
+ * count: many short chunks over long rows are faster with num_last = the longest
+ * chunk than with 0. Flagged and left as they were: a request with a malformed
  * qo_indptr pair or more tokens than keys (PKV_DEVERR_INDPTR), a seq_len outside
  * the row or past mass_stride (PKV_DEVERR_SEQ_LEN_RANGE), a negative table_idx.
  * A key on a bad page reads as zeros (PKV_DEVERR_PAGE_RANGE).
